@@ -122,9 +122,22 @@ __device__ __forceinline__ int visible_pools(int pad, int len, int q_pos, long l
 // kernel of the stream is still running; pdl_begin() makes it wait (before any global memory
 // access) until that kernel has finished and its writes are visible, then lets the next kernel
 // of the stream be scheduled. Without the launch attribute both instructions are no-ops.
-__device__ __forceinline__ void pdl_begin() {
+//
+// A kernel's const __restrict__ pointers are memory that nothing writes while it runs, so the
+// compiler moves loads through them above the wait, where that does not hold yet: the attention
+// of a prefill step read index rows that the expansion had not written (four steps in five with
+// the indices poisoned beforehand). after_wait() makes the pointers values that are known only
+// after the wait; every kernel passes the pointers that it reads through to it (or to
+// pdl_begin()) behind its wait.
+template <typename... P>
+__device__ __forceinline__ void after_wait(P &...p) {
+    (([&] { asm volatile("" : "+l"(p)::"memory"); }()), ...);
+}
+template <typename... P>
+__device__ __forceinline__ void pdl_begin(P &...p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_wait(p...);
 }
 
 template <typename... KArgs, typename... Args>

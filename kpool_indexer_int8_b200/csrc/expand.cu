@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(
     const int32_t *__restrict__ pad, const int32_t *__restrict__ len, int batch, int select_k,
     const int64_t *__restrict__ slot_map, int64_t ld_slot, int out_width,
     int32_t *__restrict__ tok_out, int32_t *__restrict__ rows_out) {
-    pdl_begin();
+    pdl_begin(topk, n_sel_in, q_seq, q_pos, pad, len, slot_map);
     __shared__ int s_nsel;
     const int n = blockIdx.y;
     const int j = blockIdx.x * blockDim.x + threadIdx.x;

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(128) index_qprep_kernel(const uint16_t *__rest
                                                           const int32_t *__restrict__ len, int batch,
                                                           int64_t ld_pools, uint16_t *__restrict__ q16,
                                                           float *__restrict__ wp, int2 *__restrict__ meta) {
-    pdl_begin();
+    pdl_begin(q_idx, w, q_seq, q_pos, pad, len);
     const int n = blockIdx.x, t = threadIdx.x, h = t >> 2, part = t & 3;
     uint4 *dst = reinterpret_cast<uint4 *>(q16 + (static_cast<int64_t>(n) * kIdxHeads + h) * kIdxDim + part * 32);
     if (n >= n_q) {   // padding of the last group
@@ -203,8 +203,7 @@ __global__ void __launch_bounds__(kGmThreads, 1) index_gemm_kernel(
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     // the query blocks, w' and meta are written by the preceding kernel
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_begin(wp, meta, pooled);
     // a wait that gives up marks the thread; it then skips its later waits (the outputs are
     // invalid and the status word says so), so that a broken pipeline ends within one wait limit
     bool ok = true;

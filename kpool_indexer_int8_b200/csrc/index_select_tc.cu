@@ -303,7 +303,10 @@ __global__ void __maxnreg__(96) index_select_tc_kernel(
     // The next kernel of the stream may launch only once this one's CTAs reach the selection (its
     // CTAs then take the SMs the finished CTAs free). Early mode: wait for the preceding kernel
     // only where its outputs are needed; otherwise at once.
-    if (!sel.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!sel.early) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        after_wait(q_idx, w, keys, key_scales, q_seq, q_pos, pad, len);
+    }
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *slots = smem + IxLayout::kSlots;

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(256) kpool_build_kernel(
     const int32_t *__restrict__ pool_begin, int batch, int max_new_pools,
     float *__restrict__ pooled, int64_t ld_pools, int32_t *__restrict__ n_pools_out,
     int8_t *__restrict__ codes, float *__restrict__ scales) {
-    pdl_begin();
+    pdl_begin(k, gate, ln_w, ln_b, pad, len, pool_begin);
     const int lane = threadIdx.x & 31;
     if (n_pools_out != nullptr && blockIdx.x == 0) {
         for (int b = threadIdx.x; b < batch; b += blockDim.x) {

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kCombineThreads) mla_combine_kernel(const floa
                                                                       const int *__restrict__ poison) {
     GLM_TL(glm_tl_combine, 0);
     GLM_TL_SMID(glm_tl_combine);
-    pdl_begin();
+    pdl_begin(part_acc, part_ml, poison);
     GLM_TL(glm_tl_combine, 1);
     __shared__ float4 part[kCombineWarps - 1][32];
     __shared__ float wts[kMaxCombineChunks];
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(128) lse_merge_kernel(const float *__restrict_
                                                         const float *__restrict__ lse_parts, int n_parts,
                                                         int n_q, int n_heads, uint16_t *__restrict__ out,
                                                         float *__restrict__ out_f32, float *__restrict__ lse) {
-    pdl_begin();
+    pdl_begin(out_parts, lse_parts);
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // n * n_heads + h
     if (item >= static_cast<int64_t>(n_q) * n_heads) return;

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kMlaThreads, 1) mla_split_tc_kernel(
     // early_q: the query block is an input no preceding kernel writes (the one-call step), so its
     // loads are issued before waiting for the preceding kernel; the row indices wait for it
     if (early_q) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    else pdl_begin();
+    else pdl_begin(q, cache, rows);
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char *Cs = smem + L::kC;
     unsigned char *Ps = smem + L::kP;
@@ -288,7 +288,10 @@ __global__ void __launch_bounds__(kMlaThreads, 1) mla_split_tc_kernel(
     qb.load(q, n, n_heads, h0, nh_real, tid);
     if (tid < NH) qmax[tid] = 0u;
     if (tid == 0) words[0] = 0u;
-    if (early_q) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (early_q) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        after_wait(cache, rows);
+    }
 
     // 2. the chunk's row indices (entries past width or outside [0, n_rows) are padding)
     int myrow = -1;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kMlaThreads, 1) mla_multi_tc_kernel(
     constexpr int kShift = (V == 32) ? 0 : (V == 16) ? 1 : 2;
     static_assert(NH % 32 == 0, "the accumulator is read and rescaled 32 heads at a time");
     if (early_q) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    else pdl_begin();
+    else pdl_begin(q, cache, rows);
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char *Cs = smem + L::kC;
     unsigned char *Ps = smem + L::kP;
@@ -594,7 +597,10 @@ __global__ void __launch_bounds__(kMlaThreads, 1) mla_multi_tc_kernel(
         lsum[tid] = 0.0f;
     }
     if (tid < 2) words[tid] = 0u;
-    if (early_q) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (early_q) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        after_wait(cache, rows);
+    }
 
     // tid < ROWS: the row of entry c ROWS + tid (-1: none, past width, or outside [0, n_rows))
     auto row_of = [&](int c) -> int {

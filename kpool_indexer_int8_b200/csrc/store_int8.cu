@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) store_int8_kernel(const uint16_t *__restr
                                                          const int64_t *__restrict__ slots,
                                                          int64_t n, int8_t *__restrict__ cache,
                                                          int64_t n_rows) {
-    pdl_begin();
+    pdl_begin(latent, slots);
     const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
          row < n; row += warps_total)
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) store_fp8_kernel(const uint16_t *__restri
                                                         const int64_t *__restrict__ slots,
                                                         int64_t n, uint8_t *__restrict__ cache,
                                                         int64_t n_rows) {
-    pdl_begin();
+    pdl_begin(latent, slots);
     const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
          row < n; row += warps_total)
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) store_fp4_kernel(const uint16_t *__restri
                                                         const int64_t *__restrict__ slots,
                                                         int64_t n, uint8_t *__restrict__ cache,
                                                         int64_t n_rows) {
-    pdl_begin();
+    pdl_begin(latent, slots);
     const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
          row < n; row += warps_total)

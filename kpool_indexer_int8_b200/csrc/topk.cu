@@ -32,7 +32,7 @@ __device__ __forceinline__ int nvis_of(const NvisSource &s, int n) {
 // ------------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) topk_hist_kernel(const float *__restrict__ scores, NvisSource src,
                                                         unsigned *__restrict__ ghist) {
-    pdl_begin();
+    pdl_begin(scores);
     __shared__ unsigned hist[kHistBins];
     const int n = blockIdx.y;
     const int n_vis = nvis_of(src, n);
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kCollectThreads) topk_collect_kernel(
     unsigned *__restrict__ ghist2, unsigned *__restrict__ counters, unsigned *__restrict__ words,
     unsigned long long *__restrict__ alist, unsigned long long *__restrict__ blist, int64_t list_cap, int select_k,
     int32_t *__restrict__ topk, int32_t *__restrict__ n_sel_out) {
-    pdl_begin();
+    pdl_begin(scores, ghist);
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SelShared &s = *reinterpret_cast<SelShared *>(smem_raw);
     __shared__ __align__(16) unsigned hist[kHistBins];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) cp_candidates_kernel(const float *__restr
                                                             const int32_t *__restrict__ topk, int select_k,
                                                             int rank, int world, float *__restrict__ cand_scores,
                                                             int32_t *__restrict__ cand_ids) {
-    pdl_begin();
+    pdl_begin(scores, topk);
     const int n = blockIdx.y;
     const int x = blockIdx.x * blockDim.x + threadIdx.x;
     if (x >= select_k) return;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kCollectThreads) merge_topk_kernel(const float
                                                                      int n_parts, int n_q, int per_part,
                                                                      int select_k, int32_t *__restrict__ topk,
                                                                      int32_t *__restrict__ n_sel) {
-    pdl_begin();
+    pdl_begin(cand_scores, cand_ids);
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SelShared &s = *reinterpret_cast<SelShared *>(smem_raw);
     const int n = blockIdx.x;
