@@ -510,12 +510,18 @@ __global__ void __maxnreg__(96) index_select_tc_kernel(
         const int n_st = min(n_st0, n_chunks);   // chunks of the sample (multi-CTA selection)
         float *xch = reinterpret_cast<float *>(smem + IxLayout::kXch);
         const bool scorer = kQ8 || qd < 2;
+        bool scales_ready = !sel.early;   // the preceding kernel's scales are safe to read
         for (int c = 0; c < n_chunks; c++) {
             const int tb = c & 1;
             const int r = kQ8 ? qd * 16 + lane : (qd & 1) * 32 + lane;   // row of the chunk
             const bool has_row = kQ8 ? lane < 16 : true;
             const int p = lo + c * kIxTile + r;
-            float ksc = 1.0f;   // the pool's int8 scale (loaded before the wait)
+            float ksc = 1.0f;   // the pool's int8 scale (loaded before the wait for its dots)
+            if (kQ8 && !scales_ready && lo + (c + 1) * kIxTile > first_new && lo + c * kIxTile < first_new + sel.new_pools) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");   // the chunk holds a pool that kernel writes
+                after_wait(key_scales);
+                scales_ready = true;
+            }
             if (kQ8 && has_row && p < hi) ksc = __ldg(key_scales + static_cast<int64_t>(b) * ld_pools + p);
             if (!tc::mbar_wait(bar(kBarAccFull + tb), (c >> 1) & 1, kIxWaitLimit)) ok = false;
             __syncwarp();

@@ -35,3 +35,21 @@ def test_step_reads_the_index_lists_of_its_own_run(cuda, chunk, fmt):
         attend(b.dims, b.q, b.cache, b.rows, b.sm_scale, alone, b.ws_mla, lse=b.lse)
         torch.cuda.synchronize()
         assert torch.equal(b.out, alone), (it, torch.nonzero((b.out != alone).flatten(1).any(1)).flatten()[:8].tolist())
+
+
+def test_step_reads_the_pool_scales_of_its_own_run(cuda):
+    # the INT8 indexer state: the scales of the pools that the step itself builds are poisoned before
+    # each run, and the scores must be those of the separate calls
+    wl = synth.custom("dependent_q8", (0, 0, 0), (6000, 64, 2048), n_heads=16, select_k=16, out_width=80, seed=45)
+    b = sdev.allocate_for(synth.generate(wl), cuda, keep_scores=True, q8=True)
+    sdev.load(synth.generate(wl), b, build_prefix=True)
+    b.ws_step[-256:].zero_()
+    P.run_stages(b)
+    torch.cuda.synchronize()
+    want, seen = b.scores.clone(), torch.isfinite(b.scores)
+    for it in range(60):
+        for s in range(len(wl.lens)):
+            b.pooled_scales[s, int(b.pool_begin[s]):] = 1e6
+        P.run_step(b)
+        torch.cuda.synchronize()
+        assert torch.equal(b.scores[seen], want[seen]), it
