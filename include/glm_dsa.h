@@ -9,6 +9,10 @@
  *   (glm_index_topk_expand -> the two above in one launch)
  *   (glm_dsa_decode_step   -> the whole step in one call)
  *   glm_sparse_mla_decode  -> sparse NoPE MLA over the gathered int8 rows (split-KV + combine)
+ * Beside it, for steps that draft several tokens and verify them at once:
+ *   glm_tree_mla_decode    -> attention of a tree of drafted tokens over the rows of its sequence
+ *   glm_block_tables       -> block tables, slots and slot maps from request lengths
+ *   glm_tree_commit        -> the accepted drafts' rows and indexer inputs into their slots
  *
  * Conventions for every entry point
  *   - Pointers named *_dev are device pointers on the current CUDA device; everything else is
@@ -393,6 +397,109 @@ int glm_mla_v_up(const glm_dsa_dims *dims, const void *o_lat_dev, const void *w_
                  float *out_v_f32_dev, void *stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* drafting several tokens: tree attention, block tables, commit                               */
+/* ------------------------------------------------------------------------------------------ */
+/*
+ * Attention of a tree of drafted tokens over the latent cache: each sequence has one index list,
+ * shared by its drafts (the draft model's layers share the indexer's selection: "GLM-5.3-Flash"
+ * pypto-lib page, indexer_share_mtp), and n_nodes drafted tokens whose latent rows lie beside the
+ * cache until they are accepted. Node i of sequence b sees
+ *   - the rows r = rows[b][x], x < row_len[b], with 0 <= r < n_rows (each entry one key; anything
+ *     else, -1 first of all, is padding): the selection of glm_index_topk_expand, or every row of
+ *     the context;
+ *   - the drafted rows j < n_tree[b] whose bit j is set in mask[b][i] (its ancestors and itself).
+ *     s = sm_scale * q[b][i][h] . c,  out[b][i][h] = sum softmax(s) c,  lse[b][i][h] = log sum exp(s)
+ * over those rows, c = code * scale being key and value (one KV head, NoPE). Nodes i >= n_tree[b],
+ * and nodes that see no row, get out = 0 and lse = -inf.
+ *   q_dev       bf16 [batch, n_nodes, n_heads, 512]     cache_dev  int8 [n_rows, 528]
+ *   rows_dev    int32 [batch, width] (may be NULL when width is 0)
+ *   row_len_dev int32 [batch] or NULL (= width); clamped to [0, width]
+ *   draft_dev   int8 [batch * n_nodes, 528]: node j of sequence b in row b * n_nodes + j (written by
+ *               glm_kv_store_int8 with those slots); rows of nodes >= n_tree[b] are not read
+ *   mask_dev    uint64 [batch, n_nodes];  n_tree_dev int32 [batch] or NULL (= n_nodes), clamped
+ *   out_dev     bf16 like q_dev;  lse_dev fp32 [batch, n_nodes, n_heads] or NULL
+ *   workspace_dev / ws_bytes: >= glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width),
+ *               256-byte aligned. Its last 256 bytes start with a status word set nonzero if a wait
+ *               on the tensor cores gave up (outputs then invalid; never cleared by the library).
+ * 1 <= n_nodes <= 64, 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with
+ * mask 1 is an ordinary decode token whose own row is not in the cache yet. A row that a node does
+ * not see has no effect on it, whatever it holds. The products run on the tensor cores with fp16
+ * operands and fp32 accumulation: codes and (scaled by powers of two) queries exactly, the softmax
+ * weights times the row scale rounded to fp16 (2^-11 relative), sums and references in fp32.
+ */
+int glm_tree_mla_decode(const glm_dsa_dims *dims, const void *q_dev, const int8_t *cache_dev, int64_t n_rows,
+                        const int32_t *rows_dev, const int32_t *row_len_dev, int32_t width,
+                        const int8_t *draft_dev, const uint64_t *mask_dev, const int32_t *n_tree_dev,
+                        int32_t batch, int32_t n_nodes, float sm_scale, void *out_dev, float *lse_dev,
+                        void *workspace_dev, size_t ws_bytes, void *stream);
+/* The same over FP8 rows (uint8 [., 528], glm_kv_store_fp8) and 4-bit rows (uint8 [., 304],
+ * glm_kv_store_fp4); cache and drafts have the same format. */
+int glm_tree_mla_decode_fp8(const glm_dsa_dims *dims, const void *q_dev, const uint8_t *cache_dev, int64_t n_rows,
+                            const int32_t *rows_dev, const int32_t *row_len_dev, int32_t width,
+                            const uint8_t *draft_dev, const uint64_t *mask_dev, const int32_t *n_tree_dev,
+                            int32_t batch, int32_t n_nodes, float sm_scale, void *out_dev, float *lse_dev,
+                            void *workspace_dev, size_t ws_bytes, void *stream);
+int glm_tree_mla_decode_fp4(const glm_dsa_dims *dims, const void *q_dev, const uint8_t *cache_dev, int64_t n_rows,
+                            const int32_t *rows_dev, const int32_t *row_len_dev, int32_t width,
+                            const uint8_t *draft_dev, const uint64_t *mask_dev, const int32_t *n_tree_dev,
+                            int32_t batch, int32_t n_nodes, float sm_scale, void *out_dev, float *lse_dev,
+                            void *workspace_dev, size_t ws_bytes, void *stream);
+
+/*
+ * Block tables, slots and slot maps of a step from request lengths. The cache is pool_blocks blocks
+ * of block_size rows; request b holds n_blocks[b] of them, block_table[b][0 .. n_blocks[b]), for its
+ * len[b] tokens, and this step appends n_new[b] tokens (0: none; below 0: the request ends and
+ * returns its blocks). Row of its token at position t (0 = its first token):
+ *     slot(b, t) = block_table[b][t / block_size] * block_size + t % block_size.
+ * New blocks come from the top of a stack, free[0 .. n_free): in request order, request b takes
+ *     need[b] = max(0, ceil((len[b] + n_new[b]) / block_size) - n_blocks[b])
+ * blocks, its j-th being free[n_free - 1 - off[b] - j] with off[b] the sum of need over the requests
+ * before it. A request is refused -- it takes nothing, its numbers stay, its tokens become padding --
+ * when need[b] > 0 and off[b] + need[b] > n_free, when its tokens run past n_cap or (with a slot
+ * map) its positions past ld_slot, when it needs more than ld_blocks blocks, or when its numbers are
+ * not those of a request (len < 0, pad < 0, n_blocks outside [0, ld_blocks], len > n_blocks * block_size).
+ *   len, n_new, n_blocks  int32 [batch];  pad int32 [batch] or NULL (= 0): left padding
+ *   block_table  int32 [batch, ld_blocks], in and out: the entries of new blocks are written, nothing else
+ *   free, n_free int32 [free_cap], [1] (n_free clamped to [0, free_cap])
+ *   slots int64 [n_cap], q_seq, q_pos int32 [n_cap]: the new tokens packed in request order: slot, request
+ *         and position pad + t; -1 for the tokens of refused requests and behind the last token; a
+ *         slot is -1 too where its block's id is outside [0, pool_blocks). Slots feed glm_kv_store_*,
+ *         q_seq / q_pos the index entry points.
+ *   slot_map     int64 [batch, ld_slot] or NULL, in and out: slot_map[b][pad + t] of the new tokens
+ *   len_out, n_blocks_out  int32 [batch] (0 of ended requests);  cu_new int32 [batch + 1]: packed offsets
+ *         (every n_new > 0 counts, refused or not; saturates at INT32_MAX)
+ *   free_out, n_free_out   int32 [free_cap], [1]: what is left of the stack, then the blocks of ended
+ *         requests in request order (entries past n_free_out are not written)
+ * The outputs (other than block_table and slot_map) must not be the inputs: CTAs read what others
+ * write. Calling again with the same inputs gives the same outputs. 0 <= batch <= 8192,
+ * 1 <= block_size <= 65536, pool_blocks * block_size <= INT32_MAX (cache rows are int32 in index lists).
+ */
+int glm_block_tables(const int32_t *len_dev, const int32_t *n_new_dev, const int32_t *n_blocks_dev,
+                     const int32_t *pad_dev, int32_t batch, int32_t block_size, int32_t *block_table_dev,
+                     int64_t ld_blocks, const int32_t *free_dev, const int32_t *n_free_dev, int32_t free_cap,
+                     int32_t pool_blocks, int64_t *slots_dev, int32_t *q_seq_dev, int32_t *q_pos_dev,
+                     int64_t n_cap, int64_t *slot_map_dev, int64_t ld_slot, int32_t *len_out_dev,
+                     int32_t *n_blocks_out_dev, int32_t *cu_new_dev, int32_t *free_out_dev,
+                     int32_t *n_free_out_dev, void *stream);
+
+/*
+ * The accepted drafts into the cache. Token i of a step packed by glm_block_tables, of request
+ * b = q_seq[i], is the request's j-th accepted draft, j = i - cu_new[b], and was node = path[b][j] of
+ * its tree: row b * n_nodes + node of draft is copied to row slots[i] of cache and, when k is given,
+ * draft_k / draft_gate[b][node] to k / gate[b][q_pos[i]] (what glm_kpool_build reads).
+ *   draft_dev, cache_dev  rows of cache_format (GLM_CACHE_*): [batch * n_nodes], [n_rows]
+ *   path_dev   int32 [batch, ld_path];  slots, q_seq, q_pos [n_cap], cu_new [batch + 1] as made
+ *   draft_k, draft_gate  bf16 [batch, n_nodes, 128] and k, gate bf16 [batch, ld_tokens, 128], or all NULL
+ * Tokens with a request, node, slot or position out of range (padding) copy nothing there. The
+ * destinations must be distinct, and draft and cache must not overlap.
+ */
+int glm_tree_commit(const glm_dsa_dims *dims, const void *draft_dev, int32_t cache_format, const int32_t *path_dev,
+                    int32_t batch, int32_t n_nodes, int64_t ld_path, const int64_t *slots_dev,
+                    const int32_t *q_seq_dev, const int32_t *q_pos_dev, const int32_t *cu_new_dev, int64_t n_cap,
+                    void *cache_dev, int64_t n_rows, const void *draft_k_dev, const void *draft_gate_dev,
+                    void *k_dev, void *gate_dev, int64_t ld_tokens, void *stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* context parallelism: one sequence's pools and rows over several ranks                        */
 /* ------------------------------------------------------------------------------------------ */
 /*
@@ -527,6 +634,7 @@ int glm_dsa_decode_step(const glm_dsa_dims *dims, const glm_dsa_step *step, void
 #define GLM_OP_TOPK_POOLS 2
 #define GLM_OP_SPARSE_MLA 3
 #define GLM_OP_DECODE_STEP 4
+#define GLM_OP_TREE_MLA 5
 
 /*
  * Bytes of device workspace an entry point needs (0 if none; (size_t)-1 for bad arguments).
@@ -534,6 +642,8 @@ int glm_dsa_decode_step(const glm_dsa_dims *dims, const glm_dsa_step *step, void
  *   GLM_OP_TOPK_POOLS:        n_q, max_pools = ld_scores, select_k
  *   GLM_OP_SPARSE_MLA:        n_q, width (max_pools and select_k unused)
  *   GLM_OP_DECODE_STEP:       n_q, max_pools = ld_pools, select_k, width = out_width
+ *   GLM_OP_TREE_MLA:          n_q = batch, select_k = n_nodes, width (max_pools unused); what a shape
+ *                             needs also serves every smaller batch, n_nodes and width
  */
 size_t glm_dsa_workspace_size(const glm_dsa_dims *dims, int32_t op, int32_t n_q,
                               int64_t max_pools, int32_t select_k, int32_t width);

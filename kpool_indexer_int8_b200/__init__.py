@@ -34,6 +34,8 @@ GLM_OP_INDEX_SCORES_TOPK = 1
 GLM_OP_TOPK_POOLS = 2
 GLM_OP_SPARSE_MLA = 3
 GLM_OP_DECODE_STEP = 4
+GLM_OP_TREE_MLA = 5
+GLM_TREE_MAX_NODES = 64
 GLM_PLAN_INDEX_MANY, GLM_PLAN_MLA_MANY, GLM_PLAN_MLA_COMBINE = 1, 2, 4
 
 EXPORTS = ("glm_check_dims", "glm_status_string", "glm_last_cuda_error", "glm_kv_store_int8",
@@ -43,7 +45,9 @@ EXPORTS = ("glm_check_dims", "glm_status_string", "glm_last_cuda_error", "glm_kv
            "glm_topk_pools", "glm_expand_selection",
            "glm_sparse_mla_decode", "glm_dsa_workspace_size", "glm_kv_store_fp8", "glm_sparse_mla_decode_fp8",
            "glm_debug_set_cross_cta_wait_limit", "glm_mla_v_up", "glm_cp_candidates", "glm_merge_topk",
-           "glm_lse_merge", "glm_kv_store_fp4", "glm_sparse_mla_decode_fp4", "glm_dsa_step_plan")
+           "glm_lse_merge", "glm_kv_store_fp4", "glm_sparse_mla_decode_fp4", "glm_dsa_step_plan",
+           "glm_tree_mla_decode", "glm_tree_mla_decode_fp8", "glm_tree_mla_decode_fp4", "glm_block_tables",
+           "glm_tree_commit")
 
 
 class glm_dsa_dims(C.Structure):
@@ -539,3 +543,150 @@ def glm_lse_merge(dims, out_parts, lse_parts, out, out_f32=None, lse=None, strea
         _dev(t, dt, nm)
     _check(lib.glm_lse_merge(C.byref(dims), _ptr(out_parts), _ptr(lse_parts), out_parts.shape[0], out_parts.shape[1],
                              _ptr(out), _ptr(out_f32), _ptr(lse), _stream(stream)), "glm_lse_merge")
+
+
+# ------------------------------------------------------------------------------------------------
+# drafting several tokens: tree attention, block tables, commit
+# ------------------------------------------------------------------------------------------------
+_TREE = [_D, _P, _P, _I64, _P, _P, _I32, _P, _P, _P, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]
+for _f in (lib.glm_tree_mla_decode, lib.glm_tree_mla_decode_fp8, lib.glm_tree_mla_decode_fp4):
+    _f.argtypes, _f.restype = _TREE, C.c_int
+lib.glm_block_tables.argtypes = [_P, _P, _P, _P, _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P, _P, _P, _I64, _P, _I64,
+                                 _P, _P, _P, _P, _P, _P]
+lib.glm_block_tables.restype = C.c_int
+lib.glm_tree_commit.argtypes = [_D, _P, _I32, _P, _I32, _I32, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64,
+                                _P]
+lib.glm_tree_commit.restype = C.c_int
+
+
+def _same_device(*tensors):
+    """The one device of the tensors given (None skipped); the library launches on the current device."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _tree_mla(name, dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree, stream, kind,
+              row_bytes):
+    for t, dt, nm, nd in ((q, torch.bfloat16, "q", 4), (cache, kind, "cache", None), (rows, torch.int32, "rows", 2),
+                          (draft, kind, "draft", None), (mask, torch.int64, "mask", 2), (out, torch.bfloat16, "out", 4),
+                          (workspace, torch.uint8, "workspace", None), (lse, torch.float32, "lse", 3),
+                          (row_len, torch.int32, "row_len", 1), (n_tree, torch.int32, "n_tree", 1)):
+        _dev(t, dt, nm, nd)
+    B, T, H = q.shape[:3]
+    _shape(q, (B, T, dims.n_heads, 512), "q")
+    _shape(out, q.shape, "out")
+    _shape(mask, (B, T), "mask")
+    _shape(rows, (B, rows.shape[1]), "rows")
+    _shape(lse, (B, T, H), "lse")
+    _shape(row_len, (B,), "row_len")
+    _shape(n_tree, (B,), "n_tree")
+    if draft.numel() != B * T * row_bytes:
+        raise ValueError(f"draft must hold {B * T} rows of {row_bytes} bytes, got {draft.numel()} bytes")
+    with torch.cuda.device(_same_device(q, cache, rows, draft, mask, out, workspace, lse, row_len, n_tree)):
+        _check(getattr(lib, name)(C.byref(dims), _ptr(q), _ptr(cache), cache.numel() // row_bytes, _ptr(rows),
+                                  _ptr(row_len), rows.shape[1], _ptr(draft), _ptr(mask), _ptr(n_tree), B, T,
+                                  float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), name)
+
+
+def glm_tree_mla_decode(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
+                        n_tree=None, stream=None) -> None:
+    """Attention of a tree of drafted tokens: q, out bf16 [B, T, n_heads, 512]; cache int8 [n_rows, 528];
+    rows int32 [B, width] (the sequence's index list, -1 padding), row_len int32 [B] or None; draft int8
+    [B * T, 528]; mask int64 [B, T] (bit j of node i: node i sees draft j), n_tree int32 [B] or None;
+    lse fp32 [B, T, n_heads] or None; workspace of GLM_OP_TREE_MLA (n_q = B, select_k = T, width)."""
+    _tree_mla("glm_tree_mla_decode", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree,
+              stream, torch.int8, GLM_ROW_BYTES)
+
+
+def glm_tree_mla_decode_fp8(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
+                            n_tree=None, stream=None) -> None:
+    """glm_tree_mla_decode over FP8 rows (cache and draft uint8 [., 528])."""
+    _tree_mla("glm_tree_mla_decode_fp8", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len,
+              n_tree, stream, torch.uint8, GLM_ROW_BYTES)
+
+
+def glm_tree_mla_decode_fp4(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
+                            n_tree=None, stream=None) -> None:
+    """glm_tree_mla_decode over 4-bit rows (cache and draft uint8 [., 304])."""
+    _tree_mla("glm_tree_mla_decode_fp4", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len,
+              n_tree, stream, torch.uint8, GLM_FP4_ROW_BYTES)
+
+
+def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_size, pool_blocks, slots, q_seq, q_pos,
+                     len_out, n_blocks_out, cu_new, free_out, n_free_out, pad=None, slot_map=None, stream=None) -> None:
+    """Block tables, slots and slot maps from request lengths: length, n_new, n_blocks (pad) int32 [B];
+    block_table int32 [B, ld_blocks]; free, free_out int32 [free_cap], n_free, n_free_out int32 [1]; slots
+    int64 / q_seq, q_pos int32 [n_cap]; len_out, n_blocks_out int32 [B]; cu_new int32 [B + 1]; slot_map
+    int64 [B, ld_slot] or None. n_new < 0 ends a request."""
+    i32, i64 = torch.int32, torch.int64
+    named = ((length, i32, "length", 1), (n_new, i32, "n_new", 1), (n_blocks, i32, "n_blocks", 1),
+             (block_table, i32, "block_table", 2), (free, i32, "free", 1), (n_free, i32, "n_free", 1),
+             (slots, i64, "slots", 1), (q_seq, i32, "q_seq", 1), (q_pos, i32, "q_pos", 1), (len_out, i32, "len_out", 1),
+             (n_blocks_out, i32, "n_blocks_out", 1), (cu_new, i32, "cu_new", 1), (free_out, i32, "free_out", 1),
+             (n_free_out, i32, "n_free_out", 1), (pad, i32, "pad", 1), (slot_map, i64, "slot_map", 2))
+    for t, dt, nm, nd in named:
+        _dev(t, dt, nm, nd)
+    B, n_cap = length.shape[0], slots.shape[0]
+    for t, nm in ((n_new, "n_new"), (n_blocks, "n_blocks"), (len_out, "len_out"), (n_blocks_out, "n_blocks_out"),
+                  (pad, "pad")):
+        _shape(t, (B,), nm)
+    _shape(block_table, (B, block_table.shape[1]), "block_table")
+    _shape(cu_new, (B + 1,), "cu_new")
+    _shape(q_seq, (n_cap,), "q_seq")
+    _shape(q_pos, (n_cap,), "q_pos")
+    _shape(free_out, free.shape, "free_out")
+    _shape(n_free, (1,), "n_free")
+    _shape(n_free_out, (1,), "n_free_out")
+    ld_slot = 0
+    if slot_map is not None:
+        ld_slot = slot_map.shape[1]
+        _shape(slot_map, (B, ld_slot), "slot_map")
+    with torch.cuda.device(_same_device(*(t for t, *_ in named))):
+        _check(lib.glm_block_tables(_ptr(length), _ptr(n_new), _ptr(n_blocks), _ptr(pad), B, int(block_size),
+                                    _ptr(block_table), block_table.shape[1], _ptr(free), _ptr(n_free), free.shape[0],
+                                    int(pool_blocks), _ptr(slots), _ptr(q_seq), _ptr(q_pos), n_cap, _ptr(slot_map),
+                                    ld_slot, _ptr(len_out), _ptr(n_blocks_out), _ptr(cu_new), _ptr(free_out),
+                                    _ptr(n_free_out), _stream(stream)), "glm_block_tables")
+
+
+def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cache, draft_k=None, draft_gate=None,
+                    k=None, gate=None, stream=None) -> None:
+    """The accepted drafts into the cache: draft rows [B * n_nodes] and cache rows [n_rows] of one format
+    (int8 528; uint8 528 or 304 by their last dimension); path int32 [B, ld_path]; slots, q_seq, q_pos,
+    cu_new of glm_block_tables; draft_k, draft_gate bf16 [B, n_nodes, 128] with k, gate bf16
+    [B, ld_tokens, 128], or none of the four."""
+    kind = draft.dtype
+    if kind not in (torch.int8, torch.uint8):
+        raise ValueError(f"draft must be int8 or uint8 rows, got {kind}")
+    named = ((draft, kind, "draft", 2), (cache, kind, "cache", None), (path, torch.int32, "path", 2),
+             (slots, torch.int64, "slots", 1), (q_seq, torch.int32, "q_seq", 1), (q_pos, torch.int32, "q_pos", 1),
+             (cu_new, torch.int32, "cu_new", 1), (draft_k, torch.bfloat16, "draft_k", 3),
+             (draft_gate, torch.bfloat16, "draft_gate", 3), (k, torch.bfloat16, "k", 3), (gate, torch.bfloat16, "gate", 3))
+    for t, dt, nm, nd in named:
+        _dev(t, dt, nm, nd)
+    B, row = path.shape[0], draft.shape[1]
+    fmt = {(torch.int8, GLM_ROW_BYTES): GLM_CACHE_INT8, (torch.uint8, GLM_ROW_BYTES): GLM_CACHE_FP8,
+           (torch.uint8, GLM_FP4_ROW_BYTES): GLM_CACHE_FP4}.get((kind, row))
+    if fmt is None or cache.shape[-1] != row:
+        raise ValueError(f"draft and cache must be rows of one format, got {kind} rows of {row} and {cache.shape[-1]}")
+    _shape(draft, (B * n_nodes, row), "draft")
+    _shape(q_seq, slots.shape, "q_seq")
+    _shape(q_pos, slots.shape, "q_pos")
+    _shape(cu_new, (B + 1,), "cu_new")
+    ld_tokens = 0 if k is None else k.shape[1]
+    for t, ld, nm in ((draft_k, n_nodes, "draft_k"), (draft_gate, n_nodes, "draft_gate"), (k, ld_tokens, "k"),
+                      (gate, ld_tokens, "gate")):
+        _shape(t, (B, ld, 128), nm)
+    with torch.cuda.device(_same_device(*(t for t, *_ in named))):
+        _check(lib.glm_tree_commit(C.byref(dims), _ptr(draft), fmt, _ptr(path), B, int(n_nodes), path.shape[1],
+                                   _ptr(slots), _ptr(q_seq), _ptr(q_pos), _ptr(cu_new), slots.shape[0], _ptr(cache),
+                                   cache.numel() // row, _ptr(draft_k), _ptr(draft_gate), _ptr(k), _ptr(gate), ld_tokens,
+                                   _stream(stream)), "glm_tree_commit")

@@ -2,9 +2,11 @@
 // kernel launches of each entry point. Nothing is enqueued unless every check passes.
 #include <cstdint>
 
+#include "block_tables.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 #include "select.cuh"
+#include "tree_mla.cuh"
 
 namespace {
 thread_local int g_last_cuda_error = 0;
@@ -158,6 +160,19 @@ size_t mla_workspace(int n_q, int n_heads, int width) {
     return mla_acc_bytes(parts) + mla_ml_bytes(parts) + 256;
 }
 
+int check_tree_shape(int32_t batch, int32_t n_nodes, int32_t width) {
+    if (batch < 0 || n_nodes < 1 || n_nodes > glm::kTreeMaxNodes || width < 0 || width > glm::kTreeMaxWidth ||
+        static_cast<int64_t>(batch) * n_nodes > 65535)
+        return GLM_ERR_INVALID_ARG;
+    return GLM_OK;
+}
+
+// Whether [p, p + bytes) and [q, q + more) share a byte (either may be null: no).
+bool overlap(const void *p, size_t bytes, const void *q, size_t more) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && bytes > 0 && more > 0 && a < b + more && b < a + bytes;
+}
+
 // Workspace of a fused step: the selection's (with its score rows), the attention's, and a
 // 256-byte status tail shared by every kernel of the step.
 struct StepLayout {
@@ -296,6 +311,11 @@ size_t glm_dsa_workspace_size(const glm_dsa_dims *dims, int32_t op, int32_t n_q,
             if (max_pools < 0 || select_k < 1 || select_k > glm::kMaxSelect || width < 1 || width > 65536)
                 return static_cast<size_t>(-1);
             return step_layout(dims, n_q, max_pools, width).total;
+        case GLM_OP_TREE_MLA: {
+            if (check_tree_shape(n_q, select_k, width) != GLM_OK) return static_cast<size_t>(-1);
+            const size_t parts = glm::tree_partials(n_q, select_k, dims->n_heads, width, num_sms());
+            return mla_acc_bytes(parts) + mla_ml_bytes(parts) + 256;
+        }
         default:
             return static_cast<size_t>(-1);
     }
@@ -586,6 +606,151 @@ int glm_sparse_mla_decode_fp4(const glm_dsa_dims *dims, const void *q, const uin
                               size_t ws_bytes, void *stream) {
     return sparse_mla_entry(dims, q, reinterpret_cast<const int8_t *>(cache), n_rows, rows, n_q, width, sm_scale,
                             out, lse, out_f32, workspace, ws_bytes, stream, glm::kFmtFp4);
+}
+
+}  // extern "C"
+
+namespace {
+int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, int64_t n_rows, const int32_t *rows,
+                   const int32_t *row_len, int32_t width, const void *draft, const uint64_t *mask,
+                   const int32_t *n_tree, int32_t batch, int32_t n_nodes, float sm_scale, void *out, float *lse,
+                   void *workspace, size_t ws_bytes, void *stream, int format) {
+    int rc = glm_check_dims(dims);
+    if (rc != GLM_OK) return rc;
+    rc = check_tree_shape(batch, n_nodes, width);
+    if (rc != GLM_OK) return rc;
+    if (n_rows < 0 || !(sm_scale == sm_scale)) return GLM_ERR_INVALID_ARG;
+    if (batch == 0) return GLM_OK;
+    if (!q || !draft || !mask || !out || (width > 0 && !rows) || (n_rows > 0 && !cache)) return GLM_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(draft, 16) || !aligned(mask, 8) || !aligned(out, 16) || (cache && !aligned(cache, 16)) ||
+        (rows && !aligned(rows, 4)) || (row_len && !aligned(row_len, 4)) || (n_tree && !aligned(n_tree, 4)) ||
+        (lse && !aligned(lse, 4)))
+        return GLM_ERR_INVALID_ARG;
+    const int H = dims->n_heads, sms = num_sms();
+    const size_t need = glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width);
+    if (workspace == nullptr || ws_bytes < need || !aligned(workspace, 256)) return GLM_ERR_WORKSPACE;
+    const size_t partials = glm::tree_partials(batch, n_nodes, H, width, sms);
+    char *ws = static_cast<char *>(workspace);
+    float *part_acc = reinterpret_cast<float *>(ws);
+    float *part_ml = reinterpret_cast<float *>(ws + mla_acc_bytes(partials));
+    glm::TreeArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.cache = static_cast<const uint8_t *>(cache);
+    a.n_rows = n_rows;
+    a.rows = rows;
+    a.row_len = row_len;
+    a.width = width;
+    a.draft = static_cast<const uint8_t *>(draft);
+    a.mask = mask;
+    a.n_tree = n_tree;
+    a.batch = batch;
+    a.n_nodes = n_nodes;
+    a.n_heads = H;
+    a.sm_scale = sm_scale;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.status = reinterpret_cast<int *>(ws + mla_acc_bytes(partials) + mla_ml_bytes(partials));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const glm::TreePlan plan = glm::tree_plan(batch, n_nodes, H, width, sms);
+    rc = cuda_status(glm::launch_tree_mla(plan, a, format, part_acc, part_ml, st));
+    if (rc != GLM_OK || plan.parts == 1) return rc;
+    return cuda_status(glm::launch_mla_combine(part_acc, part_ml, batch * n_nodes, H, plan.parts, out, nullptr, lse, st));
+}
+}  // namespace
+
+extern "C" {
+
+int glm_tree_mla_decode(const glm_dsa_dims *dims, const void *q, const int8_t *cache, int64_t n_rows,
+                        const int32_t *rows, const int32_t *row_len, int32_t width, const int8_t *draft,
+                        const uint64_t *mask, const int32_t *n_tree, int32_t batch, int32_t n_nodes, float sm_scale,
+                        void *out, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    return tree_mla_entry(dims, q, cache, n_rows, rows, row_len, width, draft, mask, n_tree, batch, n_nodes, sm_scale,
+                          out, lse, workspace, ws_bytes, stream, glm::kFmtInt8);
+}
+
+int glm_tree_mla_decode_fp8(const glm_dsa_dims *dims, const void *q, const uint8_t *cache, int64_t n_rows,
+                            const int32_t *rows, const int32_t *row_len, int32_t width, const uint8_t *draft,
+                            const uint64_t *mask, const int32_t *n_tree, int32_t batch, int32_t n_nodes,
+                            float sm_scale, void *out, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    return tree_mla_entry(dims, q, cache, n_rows, rows, row_len, width, draft, mask, n_tree, batch, n_nodes, sm_scale,
+                          out, lse, workspace, ws_bytes, stream, glm::kFmtFp8);
+}
+
+int glm_tree_mla_decode_fp4(const glm_dsa_dims *dims, const void *q, const uint8_t *cache, int64_t n_rows,
+                            const int32_t *rows, const int32_t *row_len, int32_t width, const uint8_t *draft,
+                            const uint64_t *mask, const int32_t *n_tree, int32_t batch, int32_t n_nodes,
+                            float sm_scale, void *out, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    return tree_mla_entry(dims, q, cache, n_rows, rows, row_len, width, draft, mask, n_tree, batch, n_nodes, sm_scale,
+                          out, lse, workspace, ws_bytes, stream, glm::kFmtFp4);
+}
+
+int glm_block_tables(const int32_t *len, const int32_t *n_new, const int32_t *n_blocks, const int32_t *pad,
+                     int32_t batch, int32_t block_size, int32_t *block_table, int64_t ld_blocks,
+                     const int32_t *free_list, const int32_t *n_free, int32_t free_cap, int32_t pool_blocks,
+                     int64_t *slots, int32_t *q_seq, int32_t *q_pos, int64_t n_cap, int64_t *slot_map,
+                     int64_t ld_slot, int32_t *len_out, int32_t *n_blocks_out, int32_t *cu_new, int32_t *free_out,
+                     int32_t *n_free_out, void *stream) {
+    if (batch < 0 || batch > glm::kBtMaxBatch || block_size < 1 || block_size > 65536 || ld_blocks < 0 ||
+        ld_blocks > 0x7fffffffll || free_cap < 0 || pool_blocks < 0 || n_cap < 0 || n_cap > 0x7ffffffell || ld_slot < 0 ||
+        static_cast<int64_t>(pool_blocks) * block_size > 0x7fffffffll)
+        return GLM_ERR_INVALID_ARG;
+    const bool req = batch > 0, tok = n_cap > 0;
+    if (!n_free || !n_free_out || !cu_new || (free_cap > 0 && (!free_list || !free_out)) ||
+        (tok && (!slots || !q_seq || !q_pos)) ||
+        (req && (!len || !n_new || !n_blocks || !len_out || !n_blocks_out || (ld_blocks > 0 && !block_table))))
+        return GLM_ERR_INVALID_ARG;
+    const void *words[] = {len, n_new, n_blocks, pad, block_table, free_list, n_free, q_seq, q_pos, len_out,
+                           n_blocks_out, cu_new, free_out, n_free_out};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return GLM_ERR_INVALID_ARG;
+    if (!aligned(slots, 8) || !aligned(slot_map, 8)) return GLM_ERR_INVALID_ARG;
+    // no output may be an input or another output
+    const size_t rb = static_cast<size_t>(batch) * 4, nb = static_cast<size_t>(n_cap) * 4, fb = static_cast<size_t>(free_cap) * 4;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } bufs[] = {{len_out, rb}, {n_blocks_out, rb}, {cu_new, rb + 4}, {free_out, fb}, {n_free_out, 4}, {q_seq, nb},
+                {q_pos, nb}, {slots, 2 * nb}, {block_table, rb * static_cast<size_t>(ld_blocks)},
+                {slot_map, 2 * rb * static_cast<size_t>(ld_slot)},
+                {len, rb}, {n_new, rb}, {n_blocks, rb}, {pad, rb}, {free_list, fb}, {n_free, 4}};
+    constexpr int kOutputs = 10, kAll = 16;
+    for (int i = 0; i < kOutputs; i++)
+        for (int j = i + 1; j < kAll; j++)
+            if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes)) return GLM_ERR_INVALID_ARG;
+    const glm::BlockTableArgs a{len, n_new, n_blocks, pad, batch, block_size, block_table, ld_blocks, free_list, n_free,
+                                free_cap, pool_blocks, slots, q_seq, q_pos, n_cap, slot_map, ld_slot, len_out,
+                                n_blocks_out, cu_new, free_out, n_free_out};
+    return cuda_status(glm::launch_block_tables(a, static_cast<cudaStream_t>(stream), num_sms()));
+}
+
+int glm_tree_commit(const glm_dsa_dims *dims, const void *draft, int32_t cache_format, const int32_t *path,
+                    int32_t batch, int32_t n_nodes, int64_t ld_path, const int64_t *slots, const int32_t *q_seq,
+                    const int32_t *q_pos, const int32_t *cu_new, int64_t n_cap, void *cache, int64_t n_rows,
+                    const void *draft_k, const void *draft_gate, void *k, void *gate, int64_t ld_tokens,
+                    void *stream) {
+    int rc = glm_check_dims(dims);
+    if (rc != GLM_OK) return rc;
+    if (cache_format < GLM_CACHE_INT8 || cache_format > GLM_CACHE_FP4 || batch < 0 || n_nodes < 1 ||
+        n_nodes > glm::kTreeMaxNodes || ld_path < 0 || n_cap < 0 || n_cap > 0x7fffffffll || n_rows < 0 || ld_tokens < 0)
+        return GLM_ERR_INVALID_ARG;
+    const bool state = draft_k || draft_gate || k || gate;
+    if (state && (!draft_k || !draft_gate || !k || !gate)) return GLM_ERR_INVALID_ARG;
+    if (batch == 0 || n_cap == 0) return GLM_OK;
+    if (!draft || !slots || !q_seq || !q_pos || !cu_new || (ld_path > 0 && !path) || (n_rows > 0 && !cache))
+        return GLM_ERR_INVALID_ARG;
+    const void *wide[] = {draft, cache, draft_k, draft_gate, k, gate};
+    for (const void *p : wide)
+        if (!aligned(p, 16)) return GLM_ERR_INVALID_ARG;
+    if (!aligned(path, 4) || !aligned(slots, 8) || !aligned(q_seq, 4) || !aligned(q_pos, 4) || !aligned(cu_new, 4))
+        return GLM_ERR_INVALID_ARG;
+    const int row_bytes = cache_format == GLM_CACHE_FP4 ? glm::kFp4RowBytes : glm::kRowBytes;
+    const size_t drafts = static_cast<size_t>(batch) * n_nodes;
+    if (overlap(draft, drafts * row_bytes, cache, static_cast<size_t>(n_rows) * row_bytes)) return GLM_ERR_INVALID_ARG;
+    const glm::TreeCommitArgs a{static_cast<const uint8_t *>(draft), row_bytes, path, batch, n_nodes, ld_path, slots,
+                                q_seq, q_pos, cu_new, n_cap, static_cast<uint8_t *>(cache), n_rows,
+                                static_cast<const uint16_t *>(draft_k), static_cast<const uint16_t *>(draft_gate),
+                                static_cast<uint16_t *>(k), static_cast<uint16_t *>(gate), ld_tokens};
+    return cuda_status(glm::launch_tree_commit(a, static_cast<cudaStream_t>(stream), num_sms()));
 }
 
 int glm_cp_candidates(const float *scores, int64_t ld_scores, const int32_t *topk, int32_t n_q, int32_t select_k,
