@@ -27,15 +27,19 @@ struct TreeArgs {
     int *status;
 };
 
-// How a call is cut: query rows (node, head) in tiles of `nq`, the keys of a sequence in `parts`
-// ranges; with one part the attention kernel writes the output itself.
+// How a call is cut: query rows (node, head) in tiles of `nq` (128: the two-CTA kernel), the keys of
+// a sequence in at most `parts` runs; with one part the attention kernel writes the output itself.
+// units: SMs (pairs of SMs) that take runs; levels: waves of runs that the kernel may choose from.
 struct TreePlan {
-    int nq, q_tiles, parts;
+    int nq, q_tiles, parts, units, levels;
 };
 TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms);
 // Partials (rows of 512 fp32 + 2) that a call of this shape and every smaller one may need.
 size_t tree_partials(int batch, int n_nodes, int n_heads, int width, int num_sms);
 cudaError_t launch_tree_mla(const TreePlan &plan, const TreeArgs &a, int format, float *part_acc, float *part_ml,
                             cudaStream_t stream);
+
+cudaError_t launch_tree_pair(const TreePlan &plan, const TreeArgs &a, int format, float *part_acc, float *part_ml,
+                             cudaStream_t stream);
 
 }  // namespace glm
