@@ -559,41 +559,76 @@ lib.glm_tree_commit.argtypes = [_D, _P, _I32, _P, _I32, _I32, _I64, _P, _P, _P, 
 lib.glm_tree_commit.restype = C.c_int
 
 
-def _same_device(*tensors):
-    """The one device of the tensors given (None skipped); the library launches on the current device."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+_device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _bad(t, dtype, shape, name, device):
+    """The ValueError of a tensor that failed the check of _take."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        return ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        return ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        return ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{device}")
+    return ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _tree_mla(name, dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree, stream, kind,
+def _take(device, *named):
+    """Addresses of the tensors of a call, checked: (tensor or None, dtype, shape or None, name) each, all
+    contiguous on one device. (One pass with few Python calls: the checks of a decode step's calls are
+    on its critical path. get_device() is -1 for a tensor of the CPU.)"""
+    out = []
+    for t, dtype, shape, name in named:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != device or t.dtype is not dtype or not t.is_contiguous() or \
+                (shape is not None and t.shape != shape):
+            raise _bad(t, dtype, shape or t.shape, name, device)
+        out.append(t.data_ptr())
+    return out
+
+
+def _call(fn, name, device, stream, *args):
+    """fn(*args, stream) on the device of the call's tensors (the library launches on the current one)."""
+    if device == _device_now():
+        rc = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    if rc != GLM_OK:
+        raise GlmError(rc, name)
+
+
+def _need(t, name, ndim):
+    """The shape and device of a tensor that fixes the sizes of a call."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    return t.shape, t.get_device()
+
+
+_I8, _U8, _T32, _T64, _BF = torch.int8, torch.uint8, torch.int32, torch.int64, torch.bfloat16
+
+
+def _tree_mla(fn, name, dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree, stream, kind,
               row_bytes):
-    for t, dt, nm, nd in ((q, torch.bfloat16, "q", 4), (cache, kind, "cache", None), (rows, torch.int32, "rows", 2),
-                          (draft, kind, "draft", None), (mask, torch.int64, "mask", 2), (out, torch.bfloat16, "out", 4),
-                          (workspace, torch.uint8, "workspace", None), (lse, torch.float32, "lse", 3),
-                          (row_len, torch.int32, "row_len", 1), (n_tree, torch.int32, "n_tree", 1)):
-        _dev(t, dt, nm, nd)
-    B, T, H = q.shape[:3]
-    _shape(q, (B, T, dims.n_heads, 512), "q")
-    _shape(out, q.shape, "out")
-    _shape(mask, (B, T), "mask")
-    _shape(rows, (B, rows.shape[1]), "rows")
-    _shape(lse, (B, T, H), "lse")
-    _shape(row_len, (B,), "row_len")
-    _shape(n_tree, (B,), "n_tree")
+    shape, dev = _need(q, "q", 4)
+    B, T, H, _ = shape
+    if rows.dim() != 2:
+        raise ValueError(f"rows must have 2 dims, got {rows.dim()}")
+    width, ws_bytes, per_seq = rows.shape[1], workspace.numel(), (B,)
+    p = _take(dev, (q, _BF, (B, T, dims.n_heads, 512), "q"), (cache, kind, None, "cache"), (rows, _T32, (B, width), "rows"),
+              (row_len, _T32, per_seq, "row_len"), (draft, kind, None, "draft"), (mask, _T64, (B, T), "mask"),
+              (n_tree, _T32, per_seq, "n_tree"), (out, _BF, shape, "out"), (lse, torch.float32, (B, T, H), "lse"),
+              (workspace, _U8, None, "workspace"))
     if draft.numel() != B * T * row_bytes:
         raise ValueError(f"draft must hold {B * T} rows of {row_bytes} bytes, got {draft.numel()} bytes")
-    with torch.cuda.device(_same_device(q, cache, rows, draft, mask, out, workspace, lse, row_len, n_tree)):
-        _check(getattr(lib, name)(C.byref(dims), _ptr(q), _ptr(cache), cache.numel() // row_bytes, _ptr(rows),
-                                  _ptr(row_len), rows.shape[1], _ptr(draft), _ptr(mask), _ptr(n_tree), B, T,
-                                  float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), name)
+    _call(fn, name, dev, stream, C.byref(dims), p[0], p[1], cache.numel() // row_bytes, p[2], p[3], width, p[4], p[5], p[6], B,
+          T, sm_scale, p[7], p[8], p[9], ws_bytes)
 
 
 def glm_tree_mla_decode(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
@@ -602,22 +637,22 @@ def glm_tree_mla_decode(dims, q, cache, rows, draft, mask, sm_scale, out, worksp
     rows int32 [B, width] (the sequence's index list, -1 padding), row_len int32 [B] or None; draft int8
     [B * T, 528]; mask int64 [B, T] (bit j of node i: node i sees draft j), n_tree int32 [B] or None;
     lse fp32 [B, T, n_heads] or None; workspace of GLM_OP_TREE_MLA (n_q = B, select_k = T, width)."""
-    _tree_mla("glm_tree_mla_decode", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree,
-              stream, torch.int8, GLM_ROW_BYTES)
+    _tree_mla(lib.glm_tree_mla_decode, "glm_tree_mla_decode", dims, q, cache, rows, draft, mask, sm_scale, out, workspace,
+              lse, row_len, n_tree, stream, _I8, GLM_ROW_BYTES)
 
 
 def glm_tree_mla_decode_fp8(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
                             n_tree=None, stream=None) -> None:
     """glm_tree_mla_decode over FP8 rows (cache and draft uint8 [., 528])."""
-    _tree_mla("glm_tree_mla_decode_fp8", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len,
-              n_tree, stream, torch.uint8, GLM_ROW_BYTES)
+    _tree_mla(lib.glm_tree_mla_decode_fp8, "glm_tree_mla_decode_fp8", dims, q, cache, rows, draft, mask, sm_scale, out,
+              workspace, lse, row_len, n_tree, stream, _U8, GLM_ROW_BYTES)
 
 
 def glm_tree_mla_decode_fp4(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,
                             n_tree=None, stream=None) -> None:
     """glm_tree_mla_decode over 4-bit rows (cache and draft uint8 [., 304])."""
-    _tree_mla("glm_tree_mla_decode_fp4", dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len,
-              n_tree, stream, torch.uint8, GLM_FP4_ROW_BYTES)
+    _tree_mla(lib.glm_tree_mla_decode_fp4, "glm_tree_mla_decode_fp4", dims, q, cache, rows, draft, mask, sm_scale, out,
+              workspace, lse, row_len, n_tree, stream, _U8, GLM_FP4_ROW_BYTES)
 
 
 def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_size, pool_blocks, slots, q_seq, q_pos,
@@ -626,35 +661,23 @@ def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_s
     block_table int32 [B, ld_blocks]; free, free_out int32 [free_cap], n_free, n_free_out int32 [1]; slots
     int64 / q_seq, q_pos int32 [n_cap]; len_out, n_blocks_out int32 [B]; cu_new int32 [B + 1]; slot_map
     int64 [B, ld_slot] or None. n_new < 0 ends a request."""
-    i32, i64 = torch.int32, torch.int64
-    named = ((length, i32, "length", 1), (n_new, i32, "n_new", 1), (n_blocks, i32, "n_blocks", 1),
-             (block_table, i32, "block_table", 2), (free, i32, "free", 1), (n_free, i32, "n_free", 1),
-             (slots, i64, "slots", 1), (q_seq, i32, "q_seq", 1), (q_pos, i32, "q_pos", 1), (len_out, i32, "len_out", 1),
-             (n_blocks_out, i32, "n_blocks_out", 1), (cu_new, i32, "cu_new", 1), (free_out, i32, "free_out", 1),
-             (n_free_out, i32, "n_free_out", 1), (pad, i32, "pad", 1), (slot_map, i64, "slot_map", 2))
-    for t, dt, nm, nd in named:
-        _dev(t, dt, nm, nd)
-    B, n_cap = length.shape[0], slots.shape[0]
-    for t, nm in ((n_new, "n_new"), (n_blocks, "n_blocks"), (len_out, "len_out"), (n_blocks_out, "n_blocks_out"),
-                  (pad, "pad")):
-        _shape(t, (B,), nm)
-    _shape(block_table, (B, block_table.shape[1]), "block_table")
-    _shape(cu_new, (B + 1,), "cu_new")
-    _shape(q_seq, (n_cap,), "q_seq")
-    _shape(q_pos, (n_cap,), "q_pos")
-    _shape(free_out, free.shape, "free_out")
-    _shape(n_free, (1,), "n_free")
-    _shape(n_free_out, (1,), "n_free_out")
-    ld_slot = 0
-    if slot_map is not None:
-        ld_slot = slot_map.shape[1]
-        _shape(slot_map, (B, ld_slot), "slot_map")
-    with torch.cuda.device(_same_device(*(t for t, *_ in named))):
-        _check(lib.glm_block_tables(_ptr(length), _ptr(n_new), _ptr(n_blocks), _ptr(pad), B, int(block_size),
-                                    _ptr(block_table), block_table.shape[1], _ptr(free), _ptr(n_free), free.shape[0],
-                                    int(pool_blocks), _ptr(slots), _ptr(q_seq), _ptr(q_pos), n_cap, _ptr(slot_map),
-                                    ld_slot, _ptr(len_out), _ptr(n_blocks_out), _ptr(cu_new), _ptr(free_out),
-                                    _ptr(n_free_out), _stream(stream)), "glm_block_tables")
+    per_seq, dev = _need(length, "length", 1)
+    _need(block_table, "block_table", 2)
+    B, ld_blocks = block_table.shape
+    ld_slot = 0 if slot_map is None else slot_map.shape[-1]
+    packed, pool, one = slots.shape, free.shape, (1,)
+    p = _take(dev, (length, _T32, None, "length"), (n_new, _T32, per_seq, "n_new"), (n_blocks, _T32, per_seq, "n_blocks"),
+              (pad, _T32, per_seq, "pad"), (block_table, _T32, (per_seq[0], ld_blocks), "block_table"),
+              (free, _T32, None, "free"), (n_free, _T32, one, "n_free"), (slots, _T64, None, "slots"),
+              (q_seq, _T32, packed, "q_seq"), (q_pos, _T32, packed, "q_pos"), (slot_map, _T64, (B, ld_slot), "slot_map"),
+              (len_out, _T32, per_seq, "len_out"), (n_blocks_out, _T32, per_seq, "n_blocks_out"),
+              (cu_new, _T32, (B + 1,), "cu_new"), (free_out, _T32, pool, "free_out"), (n_free_out, _T32, one, "n_free_out"))
+    _call(lib.glm_block_tables, "glm_block_tables", dev, stream, p[0], p[1], p[2], p[3], B, block_size, p[4], ld_blocks, p[5],
+          p[6], free.numel(), pool_blocks, p[7], p[8], p[9], slots.numel(), p[10], ld_slot, p[11], p[12], p[13], p[14], p[15])
+
+
+_COMMIT_FORMAT = {(torch.int8, GLM_ROW_BYTES): GLM_CACHE_INT8, (torch.uint8, GLM_ROW_BYTES): GLM_CACHE_FP8,
+                  (torch.uint8, GLM_FP4_ROW_BYTES): GLM_CACHE_FP4}
 
 
 def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cache, draft_k=None, draft_gate=None,
@@ -663,30 +686,16 @@ def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cac
     (int8 528; uint8 528 or 304 by their last dimension); path int32 [B, ld_path]; slots, q_seq, q_pos,
     cu_new of glm_block_tables; draft_k, draft_gate bf16 [B, n_nodes, 128] with k, gate bf16
     [B, ld_tokens, 128], or none of the four."""
-    kind = draft.dtype
-    if kind not in (torch.int8, torch.uint8):
-        raise ValueError(f"draft must be int8 or uint8 rows, got {kind}")
-    named = ((draft, kind, "draft", 2), (cache, kind, "cache", None), (path, torch.int32, "path", 2),
-             (slots, torch.int64, "slots", 1), (q_seq, torch.int32, "q_seq", 1), (q_pos, torch.int32, "q_pos", 1),
-             (cu_new, torch.int32, "cu_new", 1), (draft_k, torch.bfloat16, "draft_k", 3),
-             (draft_gate, torch.bfloat16, "draft_gate", 3), (k, torch.bfloat16, "k", 3), (gate, torch.bfloat16, "gate", 3))
-    for t, dt, nm, nd in named:
-        _dev(t, dt, nm, nd)
-    B, row = path.shape[0], draft.shape[1]
-    fmt = {(torch.int8, GLM_ROW_BYTES): GLM_CACHE_INT8, (torch.uint8, GLM_ROW_BYTES): GLM_CACHE_FP8,
-           (torch.uint8, GLM_FP4_ROW_BYTES): GLM_CACHE_FP4}.get((kind, row))
+    (B, ld_path), dev = _need(path, "path", 2)
+    kind, row, packed = draft.dtype, draft.shape[-1], slots.shape
+    fmt = _COMMIT_FORMAT.get((kind, row))
     if fmt is None or cache.shape[-1] != row:
         raise ValueError(f"draft and cache must be rows of one format, got {kind} rows of {row} and {cache.shape[-1]}")
-    _shape(draft, (B * n_nodes, row), "draft")
-    _shape(q_seq, slots.shape, "q_seq")
-    _shape(q_pos, slots.shape, "q_pos")
-    _shape(cu_new, (B + 1,), "cu_new")
     ld_tokens = 0 if k is None else k.shape[1]
-    for t, ld, nm in ((draft_k, n_nodes, "draft_k"), (draft_gate, n_nodes, "draft_gate"), (k, ld_tokens, "k"),
-                      (gate, ld_tokens, "gate")):
-        _shape(t, (B, ld, 128), nm)
-    with torch.cuda.device(_same_device(*(t for t, *_ in named))):
-        _check(lib.glm_tree_commit(C.byref(dims), _ptr(draft), fmt, _ptr(path), B, int(n_nodes), path.shape[1],
-                                   _ptr(slots), _ptr(q_seq), _ptr(q_pos), _ptr(cu_new), slots.shape[0], _ptr(cache),
-                                   cache.numel() // row, _ptr(draft_k), _ptr(draft_gate), _ptr(k), _ptr(gate), ld_tokens,
-                                   _stream(stream)), "glm_tree_commit")
+    drafts, state = (B, n_nodes, 128), (B, ld_tokens, 128)
+    p = _take(dev, (draft, kind, (B * n_nodes, row), "draft"), (path, _T32, None, "path"), (slots, _T64, None, "slots"),
+              (q_seq, _T32, packed, "q_seq"), (q_pos, _T32, packed, "q_pos"), (cu_new, _T32, (B + 1,), "cu_new"),
+              (cache, kind, None, "cache"), (draft_k, _BF, drafts, "draft_k"), (draft_gate, _BF, drafts, "draft_gate"),
+              (k, _BF, state, "k"), (gate, _BF, state, "gate"))
+    _call(lib.glm_tree_commit, "glm_tree_commit", dev, stream, C.byref(dims), p[0], fmt, p[1], B, n_nodes, ld_path, p[2], p[3],
+          p[4], p[5], slots.numel(), p[6], cache.numel() // row, p[7], p[8], p[9], p[10], ld_tokens)

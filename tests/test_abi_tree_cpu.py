@@ -119,6 +119,6 @@ def test_binding_checks_types_and_shapes():
     with pytest.raises(ValueError, match="CUDA"):
         kp.glm_block_tables(z(2), z(2), z(2), z(2, 4), z(9), z(1), 256, 9, z(5, dt=torch.int64), z(5), z(5), z(2), z(2),
                             z(3), z(9), z(1))
-    with pytest.raises(ValueError, match="rows"):
-        kp.glm_tree_commit(kp.make_dims(64), z(8, 528, dt=torch.float32), z(2, 4), 4, z(5, dt=torch.int64), z(5), z(5), z(3),
+    with pytest.raises(ValueError, match="CUDA"):
+        kp.glm_tree_commit(kp.make_dims(64), z(8, 528, dt=torch.int8), z(2, 4), 4, z(5, dt=torch.int64), z(5), z(5), z(3),
                            z(9, 528, dt=torch.int8))
