@@ -56,6 +56,13 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t sbo_byte
     return d;
 }
 
+// The same physical layout as an MN-major operand: rows of 128 bytes are 64 M/N elements of one K
+// index, 8 K indexes an atom; lbo_bytes between blocks of 64 M/N elements, sbo_bytes between groups
+// of 8 K indexes (advancing the start by two groups selects the next K = 16 slice).
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return desc(saddr, lbo_bytes, sbo_bytes) | static_cast<uint64_t>(2) << 61;  // SWIZZLE_128B
+}
+
 // 1-D bulk copy global -> shared completing on an mbarrier (16-byte aligned, size % 16 == 0).
 __device__ __forceinline__ void bulk_g2s(uint32_t dst_smem, const void *src, uint32_t bytes, uint32_t mbar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_smem),

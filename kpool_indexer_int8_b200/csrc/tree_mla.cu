@@ -33,9 +33,7 @@ namespace {
 
 using namespace tree;
 
-constexpr int kTrWarpWiden = 8;
-constexpr int kTrWarpMma = 16;
-constexpr int kTrThreads = 17 * 32;
+constexpr int kTrSoft = 8;                     // warps 0-7 softmax, then the widening warps and one for the tensor cores
 constexpr int kTrKeys = 64;                    // keys of a tile
 constexpr float kTrNone = -1e30f;              // reference of a query row that has seen no key
 
@@ -44,26 +42,32 @@ enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbQ = 
 template <int NQ>
 struct TrLayout {
     static constexpr int kCBytes = kTrKeys * 1024;
-    static constexpr int kC = 0;                                 // [2] tiles: 8 key groups x 64 dim groups x 128 B
+    static constexpr int kC = 0;                                 // [2] tiles: 8 blocks of 64 dims x 64 keys x 128 B, swizzled
     static constexpr int kQ = kC + 2 * kCBytes;                  // NQ/8 row groups x 64 dim groups x 128 B
     static constexpr int kPBytes = kTrKeys * 2 * NQ;
-    static constexpr int kP = kQ + NQ * 1024;                    // [2] P', core matrices of 8 keys x 8 query rows
-    static constexpr int kFac = kP + 2 * kPBytes;                // [NQ] (score factor, reference) pairs
+    static constexpr int kPBufs = NQ == 64 ? 1 : 2;              // (what else shared memory holds of 64 rows)
+    static constexpr int kP = kQ + NQ * 1024;                    // [kPBufs] P', core matrices of 8 keys x 8 query rows
+    static constexpr int kWiden = NQ == 64 ? 8 : 16;             // widening warps (64 rows: registers for their sums)
+    static constexpr int kThreads = (kTrSoft + kWiden + 1) * 32;
+    static constexpr int kGroups = NQ == 16 ? 2 : 1;             // groups of 4 rows a widening warp has in flight
+    static constexpr int kRaw = kP + kPBufs * kPBytes;           // cache rows: codes, then tails, [kWiden warps][groups][4]
+    static constexpr int kFac = kRaw + kWiden * kGroups * 4 * kRowBytes;                // [NQ] (score factor, reference) pairs
     static constexpr int kMask = kFac + NQ * 8;                  // [NQ] visibility words
     static constexpr int kOut = kMask + NQ * 8;                  // [NQ] row of the output or partial, -1: none
     static constexpr int kRed = kOut + NQ * 8;                   // [4 quadrants][NQ]
     static constexpr int kAlpha = kRed + 4 * NQ * 4;             // [NQ] factors of a rescale, at the end of the output
     static constexpr int kScl = kAlpha + NQ * 4;                 // [2][64] row scales
-    static constexpr int kMax = kScl + 2 * kTrKeys * 4;          // [2][8] largest finite scale of 8 rows
-    static constexpr int kValid = kMax + 2 * 8 * 4;              // [2][8] bytes: which rows are keys
-    static constexpr int kQmax = kValid + 16;                    // [NQ] |q| maxima (bf16 bits)
+    static constexpr int kMax = kScl + 2 * kTrKeys * 4;          // [2][16] largest finite scale of a warp's rows
+    static constexpr int kValid = kMax + 2 * 16 * 4;              // [2][64] bytes: 1 where there is a key
+    static constexpr int kQmax = kValid + 2 * kTrKeys;                    // [NQ] |q| maxima (bf16 bits)
     static constexpr int kNone = kQmax + NQ * 4;                 // query rows without a reference
     static constexpr int kBar = kNone + 8;
     static constexpr int kTmem = kBar + kTbCount * 8;
     static constexpr int kBytes = kTmem + 8;
+    static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
     static_assert(kQ % 128 == 0 && kP % 128 == 0 && kFac % 16 == 0 && kBar % 8 == 0 && kMask % 8 == 0 && kMax % 16 == 0,
                   "alignment");
-    static_assert(kBytes <= 232448, "shared memory of one CTA");
+    static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
 
 template <int V>
@@ -73,41 +77,12 @@ __device__ __forceinline__ void tr_tmem_ld(uint32_t taddr, uint32_t (&r)[V]) {
     else tc::tmem_ld32(taddr, r);
 }
 
-// What a widening thread holds of one key row: pieces 4 i + part of it (four lanes read 64
-// contiguous bytes of a row, eight lanes write 128 contiguous bytes of a core matrix).
-template <int kFmt>
-struct TrRow {
-    using R = Row<kFmt>;
-    static constexpr int kN = R::kPieces / 4;
-    uint4 v[kN];
-    uint32_t es[R::kFp4 ? kN : 1];
-    float scale;
-    int row;                                                     // cache or drafted row, -1: none
-
-    __device__ __forceinline__ void load(const uint8_t *base, int r, int part) {
-        row = r;
-        scale = R::scale(base, r);
-#pragma unroll
-        for (int i = 0; i < kN; i++) {
-            v[i] = R::codes(base, r, 4 * i + part);
-            if constexpr (R::kFp4) es[i] = R::block_scales(base, r, 4 * i + part);
-        }
-    }
-    __device__ __forceinline__ void store(unsigned char *line, int part, bool clean) const {
-#pragma unroll
-        for (int i = 0; i < kN; i++)
-#pragma unroll
-            for (int u = 0; u < R::kLines; u++)
-                *reinterpret_cast<uint4 *>(line + (R::kLines * (4 * i + part) + u) * 128) =
-                    R::line(v[i], R::kFp4 ? es[R::kFp4 ? i : 0] : 0u, u, clean);
-    }
-};
-
 template <int NQ, int kFmt>
-__global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, TreePlan plan, float *__restrict__ part_acc,
+__global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(TreeArgs a, TreePlan plan, float *__restrict__ part_acc,
                                                                  float *__restrict__ part_ml) {
     using L = TrLayout<NQ>;
     using R = Row<kFmt>;
+    constexpr int kThreads = L::kThreads, kTrWarpMma = kTrSoft + L::kWiden;
     constexpr int V = NQ / 2;                                 // query rows of a softmax thread
     constexpr int kLboP = 16 * NQ;                            // P': bytes between groups of 8 keys
     constexpr uint32_t kSCol = 4 * NQ;                        // two score accumulators after the output's 4 tiles
@@ -115,7 +90,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
     constexpr int kLow = (V == 32) ? 0 : (V == 16) ? 1 : 3;   // lane bits that repeat a query row in butterfly()
     constexpr int kShift = (V == 32) ? 0 : (V == 16) ? 1 : 2;
     pdl_begin(a.q, a.cache, a.rows, a.row_len, a.draft, a.mask, a.n_tree);
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     float2 *fac = reinterpret_cast<float2 *>(smem + L::kFac);
     uint64_t *mask = reinterpret_cast<uint64_t *>(smem + L::kMask);
     int64_t *orow = reinterpret_cast<int64_t *>(smem + L::kOut);
@@ -166,7 +142,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
             }
             return;
         }
-        for (int i = tid; i < NQ * 64; i += kTrThreads)
+        for (int i = tid; i < NQ * 64; i += kThreads)
             if (orow[i >> 6] >= 0) reinterpret_cast<uint4 *>(a.out + orow[i >> 6] * kLatent)[i & 63] = make_uint4(0u, 0u, 0u, 0u);
         if (tid < NQ && orow[tid] >= 0 && a.lse) a.lse[orow[tid]] = -INFINITY;
         return;
@@ -177,7 +153,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
         tc::fence_before_sync();
         if (lane == 0) {
             for (int i = 0; i < 2; i++) {
-                tc::mbar_init(bar(kTbFull + i), 8);
+                tc::mbar_init(bar(kTbFull + i), L::kWiden);
                 tc::mbar_init(bar(kTbDone + i), 1);
                 tc::mbar_init(bar(kTbS + i), 1);
                 tc::mbar_init(bar(kTbSFree + i), 8);
@@ -197,61 +173,95 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
         if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
     };
 
-    if (warp >= kTrWarpWiden && warp < kTrWarpMma) {
-        // ---------------- widening: row 8 w + (lane & 7) of a tile ----------------
-        const int w = warp - kTrWarpWiden, jl = lane & 7, piece = lane >> 3, k = w * 8 + jl;
+    if (warp >= kTrSoft && warp < kTrWarpMma) {
+        // ---------------- widening: keys kN w .. kN w + kN - 1 of each tile ----------------
+        // The warp's rows come into slots of its own in groups of four, each group refilled as soon as it
+        // is read; lanes 0 .. kN - 1 hold the entries of a tile's keys.
+        constexpr int kN = kTrKeys / L::kWiden, kGt = kN / 4, kG = L::kGroups;   // keys and groups of a tile
+        const int w = warp - kTrSoft;
+        unsigned char *codes = smem + L::kRaw + w * kG * 4 * R::kCodes;
+        unsigned char *tails = smem + L::kRaw + L::kWiden * kG * 4 * R::kCodes + w * kG * 4 * R::kTail;
         const int32_t *list = a.rows + static_cast<int64_t>(b) * a.width;
-        auto row_of = [&](int t) -> int {   // the cache row (or drafted row) of this thread's key of tile t, -1: none
-            if (t >= t1) return -1;
-            if (t < prefix) {
-                const int j = t * kTrKeys + k;
-                const int r = j < plen ? __ldg(list + j) : -1;
-                return (r >= 0 && r < a.n_rows) ? r : -1;
-            }
-            return k < tree_n ? b * a.n_nodes + k : -1;
+        // (An entry is looked at only when its row is needed: a test right behind the load would hold
+        // the warp until it is there.)
+        const int k = w * kN + lane;
+        auto entry_of = [&](int t) -> int {
+            if (t >= t1 || lane >= kN) return -1;
+            if (t >= prefix) return k < tree_n ? b * a.n_nodes + k : -1;
+            const int j = t * kTrKeys + k;
+            return j < plen ? __ldg(list + j) : -1;
         };
-        TrRow<kFmt> even, odd;
-        even.load(t0 < prefix ? a.cache : a.draft, row_of(t0), piece);
-        odd.load(t0 + 1 < prefix ? a.cache : a.draft, row_of(t0 + 1), piece);
-        int next = row_of(t0 + 2);
-        auto step = [&](int i, TrRow<kFmt> &row) {
+        auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
+        // starts copying group g (of four rows; kGt groups a tile, counted from the run's first); `rows`:
+        // what the lanes hold of its tile
+        auto request = [&](int g, int rows) {
+            if (g < kGt * n_tiles)
+                R::template fetch<4>(codes + g % kG * 4 * R::kCodes, tails + g % kG * 4 * R::kTail,
+                                     t0 + g / kGt < prefix ? a.cache : a.draft, rows, g % kGt * 4);
+            copy_commit();
+        };
+        // rows of tiles i .. i + 2, entries of the one after
+        int rows[3], entry;
+        {
+            int e[3];
+#pragma unroll
+            for (int u = 0; u < 3; u++) e[u] = entry_of(t0 + u);
+            entry = entry_of(t0 + 3);
+#pragma unroll
+            for (int u = 0; u < 3; u++) rows[u] = row_of(t0 + u, e[u]);
+        }
+#pragma unroll
+        for (int g = 0; g < kG; g++) request(g, rows[g / kGt]);
+        for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, buf = i & 1;
             const bool drafts = t >= prefix;
-            if (i >= 2) wait(kTbDone + buf, (i >> 1) - 1);
-            row.store(smem + L::kC + buf * L::kCBytes + w * 8192 + jl * 16, piece, drafts);
-            float sc = row.scale;
-            if (kFmt != kFmtInt8 && drafts) {   // a drafted row with NaN codes: its scale makes every score with it NaN
-                const unsigned nan = __ballot_sync(0xffffffffu, R::has_nan(a.draft, row.row, piece));
-                if ((nan >> jl) & 0x01010101u) sc = __int_as_float(0x7fc00000);
-            }
-            const unsigned valid = __ballot_sync(0xffffffffu, row.row >= 0) & 0xffu;
-            float m = fabsf(sc) < INFINITY ? sc : 0.0f;
+            const bool valid = rows[0] >= 0;
+            float sc = 0.0f;
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane < 8) scl[buf * kTrKeys + w * 8 + lane] = sc;
-            if (lane == 0) {
-                smx[buf * 8 + w] = m;
-                val[buf * 8 + w] = static_cast<uint8_t>(valid);
+            for (int h = 0; h < kGt; h++) {
+                const int g = kGt * i + h;
+                copy_wait<kG - 1>();                          // the group is there
+                unsigned char *first = codes + g % kG * 4 * R::kCodes, *tail = tails + g % kG * 4 * R::kTail;
+                if (valid && lane / 4 == h) sc = R::scale(tail + (lane & 3) * R::kTail);
+                if (kFmt != kFmtInt8 && drafts) {   // a drafted row with NaN codes: its scale makes every score with it NaN
+                    for (int r = 0; r < 4; r++)
+                        if (R::has_nan(first + r * R::kCodes, tail + r * R::kTail) && lane == h * 4 + r && valid) sc = __int_as_float(0x7fc00000);
+                    R::clean(R::kFp4 ? tail : first, 4 * (R::kFp4 ? R::kTail : R::kCodes));
+                }
+                if (h == 0 && i >= 2) wait(kTbDone + buf, (i >> 1) - 1);   // C(i - 2) has been read
+#pragma unroll 2
+                for (int r = 0; r < 4; r++) {
+                    unsigned char *to = smem + L::kC + buf * L::kCBytes + (lane >> 3) * 8192 + swizzled(w * kN + h * 4 + r, lane & 7);
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {              // lines lane and lane + 32
+                        const auto v = R::line(first + r * R::kCodes, tail + r * R::kTail, lane + 32 * u, lane / 2 + 16 * u);
+                        *reinterpret_cast<uint4 *>(to + u * 4 * 8192) = R::widen(v);
+                    }
+                }
+                __syncwarp();
+                request(g + kG, rows[(h + kG) / kGt]);
             }
+            const float m = finite_max(sc);
+            if (lane < kN) {
+                scl[buf * kTrKeys + k] = sc;
+                val[buf * kTrKeys + k] = valid ? 1 : 0;
+            }
+            if (lane == 0) smx[buf * 16 + w] = m;
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(kTbFull + buf));
-            if (i + 2 < n_tiles) {
-                row.load(t + 2 < prefix ? a.cache : a.draft, next, piece);
-                next = row_of(t + 3);
-            }
-        };
-        for (int i = 0; i < n_tiles; i += 2) {
-            step(i, even);
-            if (i + 1 < n_tiles) step(i + 1, odd);
+            rows[0] = rows[1];
+            rows[1] = rows[2];
+            rows[2] = row_of(t + 3, entry);
+            entry = entry_of(t + 4);
         }
     } else if (warp == kTrWarpMma) {
         // ---------------- tensor cores ----------------
         constexpr uint32_t id_s = tc::idesc_f16(kTrKeys, NQ, false, false);
         constexpr uint32_t id_o = tc::idesc_f16(128, NQ, true, true);
         const uint64_t dq = tc::desc(tc::smem_addr(smem + L::kQ), 128, 8192);
-        const uint64_t dc = tc::desc(tc::smem_addr(smem + L::kC), 128, 8192);
-        const uint64_t dct = tc::desc(tc::smem_addr(smem + L::kC), 8192, 128);
+        const uint64_t dc = tc::desc_sw128(tc::smem_addr(smem + L::kC), 1024);
+        const uint64_t dct = tc::desc_sw128_mn(tc::smem_addr(smem + L::kC), 8192, 1024);
         const uint64_t dp = tc::desc(tc::smem_addr(smem + L::kP), kLboP, 128);
         auto accumulate = [&](int i) {   // O^T += C(i)^T P(i)^T: M = 128 latent dims of 4 tiles, K = 64 keys
             const int buf = i & 1;
@@ -259,12 +269,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
             if (tc::elect_one()) {
-                const uint64_t ca = dct + ((buf * L::kCBytes) >> 4), pa = dp + ((buf * L::kPBytes) >> 4);
+                const uint64_t ca = dct + ((buf * L::kCBytes) >> 4), pa = dp + (((i % L::kPBufs) * L::kPBytes) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < kTrKeys / 16; ks++)
 #pragma unroll
                     for (int mt = 0; mt < kLatent / 128; mt++)
-                        tc::mma_bf16(tmem + mt * NQ, ca + ((ks * 2 * 8192 + mt * 2048) >> 4), pa + ((ks * 2 * kLboP) >> 4),
+                        tc::mma_bf16(tmem + mt * NQ, ca + ((ks * 2048 + mt * 2 * 8192) >> 4), pa + ((ks * 2 * kLboP) >> 4),
                                      id_o, (i > 0 || ks > 0) ? 1u : 0u);
                 tc::mma_commit(bar(kTbDone + buf));
             }
@@ -281,7 +291,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
                 const uint64_t ca = dc + ((buf * L::kCBytes) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < kLatent / 16; ks++)
-                    tc::mma_bf16(tmem + kSCol + buf * NQ, ca + ((ks * 256) >> 4), dq + ((ks * 256) >> 4), id_s,
+                    tc::mma_bf16(tmem + kSCol + buf * NQ, ca + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
+                                 dq + ((ks * 256) >> 4), id_s,
                                  ks > 0 ? 1u : 0u);
                 tc::mma_commit(bar(kTbS + buf));
             }
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
             wait(kTbS + buf, i >> 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
-            const bool key = lane < 16 && ((val[buf * 8 + (j >> 3)] >> (j & 7)) & 1);
+            const bool key = lane < 16 && val[buf * kTrKeys + j] != 0;
             const float sc = key ? scl[buf * kTrKeys + j] : 0.0f;
             // the scores of this thread's key less the references (0 for a row that has none)
             float x[V];
@@ -360,12 +371,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
                 for (int e = 0; e < V; e++)
                     if (!key || !((mask[c0 + e] >> j) & 1ull)) x[e] = -INFINITY;   // what each node sees of the drafts
             }
-            const float4 ma = *reinterpret_cast<const float4 *>(smx + buf * 8), mb = *reinterpret_cast<const float4 *>(smx + buf * 8 + 4);
-            const float smax = fmaxf(fmaxf(fmaxf(ma.x, ma.y), fmaxf(ma.z, ma.w)), fmaxf(fmaxf(mb.x, mb.y), fmaxf(mb.z, mb.w)));
+            float smax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < L::kWiden / 4; e++) {
+                const float4 v = reinterpret_cast<const float4 *>(smx + buf * 16)[e];
+                smax = max3(smax, fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int e = 0; e < V; e++) top = fmaxf(top, x[e]);
-            const bool grow = smax > 16.0f * sigma;               // (sigma 0: no scale yet)
+            const bool grow = smax > kSpread * sigma;               // (sigma 0: no scale yet)
             if (named_or(1, 256, top > kGrow) || grow || pending) {
                 // move the references and sigma, and rescale what they scale
                 float m[V];
@@ -419,8 +434,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
                 named_sync(1, 256);                               // (the arrays are free again)
             }
             const float ratio = sigma > 0.0f ? sc * (kBoost / sigma) : sc;   // (sigma 0: every finite scale is 0)
-            if (i >= 2) wait(kTbDone + buf, (i >> 1) - 1);        // P(i - 2) has been read
-            unsigned char *line = smem + L::kP + buf * L::kPBytes + (j >> 3) * kLboP + (c0 >> 3) * 128 + (j & 7) * 16;
+            if (i >= L::kPBufs)                                   // P(i - kPBufs) has been read
+                wait(kTbDone + ((i - L::kPBufs) & 1), (i - L::kPBufs) >> 1);
+            unsigned char *line = smem + L::kP + (i % L::kPBufs) * L::kPBytes + (j >> 3) * kLboP + (c0 >> 3) * 128 + (j & 7) * 16;
 #pragma unroll
             for (int g = 0; g < V / 8; g++) {
                 uint32_t p4[4];
@@ -505,10 +521,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_mla_kernel(TreeArgs a, Tre
 template <int NQ, int kFmt>
 cudaError_t launch_tree_t(const TreePlan &p, const TreeArgs &a, float *part_acc, float *part_ml, cudaStream_t stream) {
     auto kernel = tree_mla_kernel<NQ, kFmt>;
-    const int smem = TrLayout<NQ>::kBytes;
+    const int smem = TrLayout<NQ>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, dim3(a.batch, p.parts), dim3(kTrThreads), smem, stream, a, p, part_acc, part_ml);
+    e = launch_pdl(kernel, dim3(a.batch, p.parts), dim3(TrLayout<NQ>::kThreads), smem, stream, a, p, part_acc, part_ml);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -526,7 +542,7 @@ TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms) 
     p.nq = rows <= 16 ? 16 : (rows <= 32 ? 32 : (pair ? 128 : 64));
     p.q_tiles = pair ? (rows + 127) / 128 : 1;
     p.units = pair ? num_sms / 2 : num_sms;
-    const long long tiles = tree_tiles(width, pair ? 128 : kTrKeys), base = static_cast<long long>(batch) * p.q_tiles;
+    const long long tiles = tree_tiles(width, pair ? kTreePairKeys : kTrKeys), base = static_cast<long long>(batch) * p.q_tiles;
     // one wave of runs when the lists are short (or there is one); else the kernel weighs up to four
     // against the lists' lengths
     p.levels = batch > 1 && base * tiles > 32ll * p.units ? kTrLevels : 1;

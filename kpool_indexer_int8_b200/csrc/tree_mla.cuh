@@ -9,6 +9,7 @@ namespace glm {
 
 constexpr int kTreeMaxNodes = 64;             // one word of visibility bits per node
 constexpr int kTreeMaxWidth = 1 << 20;        // index entries of a sequence
+constexpr int kTreePairKeys = 96;             // keys of a tile of the two-CTA kernel
 
 struct TreeArgs {
     const uint16_t *q;              // bf16 [batch][n_nodes][n_heads][512]

@@ -10,8 +10,9 @@ namespace glm {
 namespace tree {
 
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr float kGrow = 8.0f;                  // a score passes its reference by at most 2^8
-constexpr float kBoost = 8.0f;                 // P' <= 2^8 * 16 * 8 = 2^15 < 65504
+constexpr float kGrow = 12.0f;                 // a score passes its reference by at most 2^12
+constexpr float kSpread = 2.0f;                // a row scale is at most 2 sigma
+constexpr float kBoost = 4.0f;                 // P' <= 2^12 * 2 * 4 = 2^15 < 65504
 
 // The keys of a sequence in tiles: the index list's, then one tile of drafted rows.
 __device__ __forceinline__ int list_len(const TreeArgs &a, int b) {
@@ -65,65 +66,145 @@ __device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, i
     return best;
 }
 
-// 16-byte pieces of a cache row of one of the formats, widened to fp16 (exact): 16 int8 or E4M3
-// codes are two lines of 8 dims, 32 E2M1 codes (with two block scales) four.
+// Starts copying 16 bytes to shared memory, or zeroes them there (`there` false: nothing is read).
+__device__ __forceinline__ void copy16(void *to_smem, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_addr(to_smem)), "l"(from), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most kNewer of the groups committed last are still in flight; for the whole warp.
+template <int kNewer>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kNewer) : "memory");
+    __syncwarp();
+}
+// 0x80 in each byte that is an E4M3 NaN (0x7f, 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// Cache rows of one of the formats, as a widening warp takes them. A row is copied whole into shared
+// memory by one asynchronous 16-byte copy per lane (eight warps gather rows at 21 to 27 bytes a cycle
+// and SM this way, 21 to 24 by bulk copies, whose issue takes 90 cycles a row, 19 to 24 by loads into
+// registers); then each lane widens lines of 8 dims of it to fp16 (exact): 8 bytes of int8 or E4M3
+// codes, 4 bytes of E2M1 codes with the block scale of their 16 dims.
 template <int kFmt>
 struct Row {
     static constexpr bool kFp4 = kFmt == kFmtFp4;
     static constexpr int kBytes = kFp4 ? kFp4RowBytes : kRowBytes;
-    static constexpr int kSclAt = kFp4 ? kFp4RowScaleAt : kLatent;
-    static constexpr int kPieces = kFp4 ? 16 : 32;          // of a row
-    static constexpr int kLines = kFp4 ? 4 : 2;             // lines of 8 dims of a piece
+    static constexpr int kCodes = kFp4 ? 256 : 512;         // bytes of codes, then the tail with the scales
+    static constexpr int kTail = kBytes - kCodes;
+    static constexpr int kSclAt = (kFp4 ? kFp4RowScaleAt : kLatent) - kCodes;   // the row scale in the tail
 
-    __device__ __forceinline__ static const uint8_t *at(const uint8_t *base, int64_t r) { return base + r * kBytes; }
-    __device__ __forceinline__ static float scale(const uint8_t *base, int64_t r) {
-        return r >= 0 ? __ldg(reinterpret_cast<const float *>(at(base, r) + kSclAt)) : 0.0f;
+    // One warp starts copying the NR rows that lanes lane0 .. lane0 + NR - 1 hold (-1: zeros) to codes
+    // [NR][kCodes] and tails [NR][kTail] in shared memory. No branch, so that the copies go out back to back.
+    template <int NR>
+    __device__ __forceinline__ static void fetch(unsigned char *codes, unsigned char *tails, const uint8_t *base, int rows,
+                                                 int lane0) {
+        constexpr int kPer = 512 / kCodes, kTp = kTail / 16;      // rows of a copy, pieces of a tail
+        static_assert(NR % kPer == 0 && NR <= 32, "rows of a group");
+        const int lane = threadIdx.x & 31, at = (lane * 16) % kCodes;
+        int r[NR / kPer];
+#pragma unroll
+        for (int i = 0; i < NR / kPer; i++) r[i] = __shfl_sync(0xffffffffu, rows, lane0 + i * kPer + lane * 16 / kCodes);
+#pragma unroll
+        for (int i = 0; i < NR / kPer; i++)
+            copy16(codes + i * 512 + lane * 16, base + static_cast<int64_t>(max(r[i], 0)) * kBytes + at, r[i] >= 0);
+#pragma unroll
+        for (int i = 0; i < NR * kTp; i += 32) {
+            const int p = i + lane, rt = __shfl_sync(0xffffffffu, rows, lane0 + min(p / kTp, NR - 1));
+            if (p < NR * kTp) copy16(tails + p * 16, base + static_cast<int64_t>(max(rt, 0)) * kBytes + kCodes + p % kTp * 16, rt >= 0);
+        }
     }
-    __device__ __forceinline__ static uint4 codes(const uint8_t *base, int64_t r, int k) {
-        return r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(at(base, r)) + k) : make_uint4(0u, 0u, 0u, 0u);
+    // The same for the codes of dims 128 part + [0, 128) of each 256 (half a row: 256 or 128 bytes of
+    // codes, both parts of a row behind each other), and the whole tails of 4-bit rows.
+    template <int NR>
+    __device__ __forceinline__ static void fetch_half(unsigned char *codes, unsigned char *tails, const uint8_t *base, int rows,
+                                                      int part) {
+        constexpr int kHalf = kCodes / 2, kPer = 512 / kHalf, kSeg = kHalf / 2;
+        static_assert(NR % kPer == 0 && NR <= 32, "rows of a group");
+        const int lane = threadIdx.x & 31, in = (lane * 16) % kHalf;
+        const int at = (in / kSeg) * kHalf + part * kSeg + in % kSeg;
+        int r[NR / kPer];
+#pragma unroll
+        for (int i = 0; i < NR / kPer; i++) r[i] = __shfl_sync(0xffffffffu, rows, i * kPer + lane * 16 / kHalf);
+#pragma unroll
+        for (int i = 0; i < NR / kPer; i++)
+            copy16(codes + i * 512 + lane * 16, base + static_cast<int64_t>(max(r[i], 0)) * kBytes + at, r[i] >= 0);
+        if constexpr (kFp4) {
+#pragma unroll
+            for (int i = 0; i < NR * 3; i += 32) {
+                const int p = i + lane, rt = __shfl_sync(0xffffffffu, rows, min(p / 3, NR - 1));
+                if (p < NR * 3) copy16(tails + p * 16, base + static_cast<int64_t>(max(rt, 0)) * kBytes + kCodes + p % 3 * 16, rt >= 0);
+            }
+        }
     }
-    __device__ __forceinline__ static uint32_t block_scales(const uint8_t *base, int64_t r, int k) {
-        return r >= 0 ? __ldg(reinterpret_cast<const uint16_t *>(at(base, r) + kFp4ScalesAt) + k) : 0u;
+    __device__ __forceinline__ static float scale(const unsigned char *tail) { return *reinterpret_cast<const float *>(tail + kSclAt); }
+
+    // Line `l` of codes as it lies there (block: which 16 dims of the row it belongs to), and as 8 fp16
+    // values.
+    struct Line {
+        uint2 codes;
+        uint32_t es;
+    };
+    __device__ __forceinline__ static Line line(const unsigned char *codes, const unsigned char *tail, int l, int block) {
+        Line v;
+        if constexpr (kFp4) {
+            v.codes = make_uint2(reinterpret_cast<const uint32_t *>(codes)[l], 0u);
+            v.es = tail[block];
+        } else {
+            v.codes = reinterpret_cast<const uint2 *>(codes)[l];
+            v.es = 0u;
+        }
+        return v;
     }
-    // Line u of piece v (block scales es) as 8 fp16 values; clean: NaN codes become zeros.
-    __device__ __forceinline__ static uint4 line(const uint4 &v, uint32_t es, int u, bool clean) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __device__ __forceinline__ static uint4 widen(const Line &v) {
         uint32_t o[4];
         if constexpr (kFp4) {
-            const __half2_raw sc = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(es), __NV_E4M3);
-            fp4_to_f16x8(w[u], static_cast<uint32_t>(u < 2 ? sc.x : sc.y) * 0x10001u, o);
+            const __half_raw sc = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(v.es), __NV_E4M3);
+            fp4_to_f16x8(v.codes.x, static_cast<uint32_t>(sc.x) * 0x10001u, o);
         } else if constexpr (kFmt == kFmtFp8) {
-            fp8_to_f16x4(w[2 * u], o[0], o[1]);
-            fp8_to_f16x4(w[2 * u + 1], o[2], o[3]);
+            fp8_to_f16x4(v.codes.x, o[0], o[1]);
+            fp8_to_f16x4(v.codes.y, o[2], o[3]);
         } else {
-            codes_to_f16x4(w[2 * u], o[0], o[1]);
-            codes_to_f16x4(w[2 * u + 1], o[2], o[3]);
-        }
-        if constexpr (kFmt != kFmtInt8) {
-            if (clean) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if ((o[i] & 0x7fffu) > 0x7c00u) o[i] &= 0xffff0000u;
-                    if ((o[i] & 0x7fff0000u) > 0x7c000000u) o[i] &= 0x0000ffffu;
-                }
-            }
+            codes_to_f16x4(v.codes.x, o[0], o[1]);
+            codes_to_f16x4(v.codes.y, o[2], o[3]);
         }
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
-    // Whether a row holds a NaN code (E4M3 codes or block scales of 0x7f / 0xff), looked for by the
-    // four lanes that share it (part 0 .. 3); int8 codes have none.
-    __device__ __forceinline__ static bool has_nan(const uint8_t *base, int64_t r, int part) {
+    // One warp makes zeros of the NaN codes of n bytes (a multiple of 16) of rows in shared memory: of E4M3
+    // codes, or of 4-bit rows' tails, [rows][kTail], whose first 32 bytes are block scales.
+    __device__ __forceinline__ static void clean(unsigned char *bytes, int n) {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll 1
+        for (int i = lane * 4; i < n; i += 128) {
+            if (kFp4 && i % kTail >= 32) continue;
+            uint32_t *w = reinterpret_cast<uint32_t *>(bytes + i);
+            const uint32_t m = nan_bytes(*w);
+            if (m) *w &= ~((m >> 7) * 0xffu);
+        }
+        __syncwarp();
+    }
+    // Whether this lane's share of a row holds a NaN code (E4M3 codes or block scales of 0x7f / 0xff).
+    // Int8 codes have none.
+    __device__ __forceinline__ static bool nan_share(const unsigned char *codes, const unsigned char *tail) {
         if constexpr (kFmt == kFmtInt8) return false;
-        if (r < 0) return false;
-        bool nan = false;
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(at(base, r) + (kFp4 ? kFp4ScalesAt : 0));
-        for (int i = part; i < (kFp4 ? 8 : 128); i += 4) {
-            const uint32_t v = __ldg(w + i) & 0x7f7f7f7fu;
-            nan |= ((v + 0x01010101u) & 0x80808080u) != 0u;
+        const int lane = threadIdx.x & 31;
+        auto bad = [](uint32_t x) { return nan_bytes(x) != 0u; };
+        bool nan;
+        if constexpr (kFp4) {
+            nan = lane < 8 && bad(reinterpret_cast<const uint32_t *>(tail)[lane]);
+        } else {
+            const uint4 v = reinterpret_cast<const uint4 *>(codes)[lane];
+            nan = bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
         }
         return nan;
     }
+    __device__ __forceinline__ static bool has_nan(const unsigned char *codes, const unsigned char *tail) {
+        return __any_sync(0xffffffffu, nan_share(codes, tail));
+    }
 };
+// Where line c (of 8) of row r goes in a block of 64 dims, rows of 128 bytes in the 128-byte swizzle:
+// eight lanes that write the lines of a row write eight different banks.
+__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -145,6 +226,38 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two fp32 values in one 64-bit register, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) { return pack2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The largest finite value >= 0 of a warp (row scales; 0 if there is none).
+__device__ __forceinline__ float finite_max(float v) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u));
 }
 // The power of two that puts a bf16 magnitude (its bits) in [2^14, 2^15): bf16 values so scaled are
 // exact in fp16 (those below 2^-17 of the range aside).

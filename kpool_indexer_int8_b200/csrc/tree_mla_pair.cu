@@ -22,57 +22,58 @@ namespace {
 
 using namespace tree;
 
-constexpr int kPrWarpWiden = 4;
-constexpr int kPrWarpMma = 12;
-constexpr int kPrThreads = 13 * 32;
+constexpr int kPrSoft = 4, kPrK = 4, kPrV = 6; // warps 0-3 softmax, 4-7 K, 8-13 V, 14 tensor cores
+constexpr int kPrWarpV = kPrSoft + kPrK, kPrWarpMma = kPrWarpV + kPrV;
+constexpr int kPrThreads = (kPrWarpMma + 1) * 32;
 constexpr int kPrRows = 64;                    // query rows of a CTA
-constexpr int kPrKeys = 128;                   // keys of a tile
+constexpr int kPrKeys = kTreePairKeys;         // keys of a tile
+constexpr int kPrHalf = kPrKeys / 2;           // keys of a CTA's K
+constexpr int kPrKn = kPrHalf / kPrK;          // keys of a K warp, of each half of a tile
+constexpr int kPrVn = kPrKeys / kPrV;          // keys of a V warp
 constexpr int kPrMeta = 3;                     // tiles whose scales are kept
-constexpr uint32_t kPrSCol = 256;              // two score accumulators of 64 columns after the output's 256
+constexpr uint32_t kPrSCol = 256;              // two score accumulators of 48 columns after the output's 256
+constexpr uint32_t kPrSStep = 64;
 
 enum PrBar { kPbQ = 0, kPbK, kPbV, kPbP, kPbSFree, kPbS = 6, kPbDone = 8, kPbMeta = 10, kPbCount = 13 };
 
 struct PrLayout {
     static constexpr int kQ = 0;                                 // 8 row groups x 64 dim groups x 128 B
-    static constexpr int kK = kQ + kPrRows * 1024;               // 8 key groups x 64 dim groups x 128 B
-    static constexpr int kV = kK + 64 * 1024;                    // 16 key groups x 32 own dim groups x 128 B
-    static constexpr int kP = kV + kPrKeys * 512;                // 8 row groups x 16 key groups x 128 B
-    static constexpr int kScl = kP + kPrRows * kPrKeys * 2;      // [3][128] row scales
-    static constexpr int kMax = kScl + kPrMeta * kPrKeys * 4;    // [3][16] largest finite scale of 8 keys
-    static constexpr int kValid = kMax + kPrMeta * 16 * 4;       // [3][16] bytes: which rows are keys
-    static constexpr int kRed = kValid + kPrMeta * 16;           // [128]
+    static constexpr int kKBlock = kPrHalf * 128;                // a block of 64 dims of K, of V
+    static constexpr int kVBlock = kPrKeys * 128;
+    static constexpr int kK = kQ + kPrRows * 1024;               // 8 blocks of 64 dims x 48 keys x 128 B, swizzled
+    static constexpr int kV = kK + 8 * kKBlock;                  // 4 blocks of 64 own dims x 96 keys x 128 B, swizzled
+    static constexpr int kPGroup = kPrKeys * 16;                 // 8 rows of P'
+    static constexpr int kP = kV + 4 * kVBlock;                  // 8 row groups x 12 key groups x 128 B
+    static constexpr int kRawK = kP + 8 * kPGroup;               // the 48 own keys' rows: codes, then tails
+    static constexpr int kRawV = kRawK + kPrHalf * kRowBytes;    // the own dims of 96 rows: codes, then tails of 4-bit rows
+    static constexpr int kScl = kRawV + kPrKeys * 256;           // [3][96] row scales
+    static constexpr int kMax = kScl + kPrMeta * kPrKeys * 4;    // [3][8] largest finite scale of a K warp's keys (4 used)
+    static constexpr int kValid = kMax + kPrMeta * 8 * 4;       // [3][96] bytes: 1 where there is a key
+    static constexpr int kFull = kValid + kPrMeta * kPrKeys;     // [3][2][8] bytes: 1 where a K warp's keys are all there
+    static constexpr int kRed = kFull + kPrMeta * 16;            // [2][64]
     static constexpr int kRowK = kRed + 128 * 4;                 // [64] score factors
     static constexpr int kBar = kRowK + kPrRows * 4;
     static constexpr int kTmem = kBar + kPbCount * 8;
     static constexpr int kBytes = kTmem + 8;
-    static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 16 == 0, "alignment");
-    static_assert(kBytes <= 232448, "shared memory of one CTA");
+    static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
+    static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 8 == 0 && kFull % 16 == 0 && kMax % 16 == 0 && kK % 1024 == 0 &&
+                      kV % 1024 == 0 && kKBlock % 1024 == 0 && kVBlock % 1024 == 0 && kRawK % 128 == 0 && kRawV % 128 == 0, "alignment");
+    static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// One arrival on a barrier of the pair's first CTA.
+// One arrival on a barrier of the pair's first CTA. What it announces stays in the arriving CTA (operands
+// in its shared memory, behind a proxy fence, and tensor memory, behind a tcgen05 fence), so the
+// arrival needs no ordering across the cluster: with release at cluster scope each of the four
+// arrivals of a tile waited 900 to 1,400 cycles for the warp's outstanding memory traffic.
 __device__ __forceinline__ void arrive_leader(uint32_t mbar) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\t"
         "mapa.shared::cluster.u32 r, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}\n" ::"r"(mbar)
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}\n" ::"r"(mbar)
         : "memory");
-}
-__device__ __forceinline__ bool cluster_wait(uint32_t mbar, uint32_t parity, uint32_t limit) {
-    for (uint32_t i = 0; i < limit; i++) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(ok)
-            : "r"(mbar), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    return false;
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -95,10 +96,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     using L = PrLayout;
     using R = Row<kFmt>;
     pdl_begin(a.q, a.cache, a.rows, a.row_len, a.draft, a.mask, a.n_tree);
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     float *scl = reinterpret_cast<float *>(smem + L::kScl);
     float *smx = reinterpret_cast<float *>(smem + L::kMax);
-    uint8_t *val = reinterpret_cast<uint8_t *>(smem + L::kValid);
+    uint8_t *val = smem + L::kValid, *full = smem + L::kFull;
     float *red = reinterpret_cast<float *>(smem + L::kRed);
     float *rowk = reinterpret_cast<float *>(smem + L::kRowK);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmem);
@@ -144,22 +146,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
         return;
     }
+    if (tid < kPrMeta * 8) smx[tid] = 0.0f;                   // (what no K warp writes)
+    if (tid < kPrMeta * 16) full[tid] = 1;
     if (warp == kPrWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_addr(tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc::fence_before_sync();
         if (lane == 0) {
-            tc::mbar_init(bar(kPbQ), 8);                      // (both CTAs' warps arrive at the first's)
-            tc::mbar_init(bar(kPbK), 16);
-            tc::mbar_init(bar(kPbV), 16);
-            tc::mbar_init(bar(kPbP), 8);
+            tc::mbar_init(bar(kPbQ), 2 * kPrSoft);                      // (both CTAs' warps arrive at the first's)
+            tc::mbar_init(bar(kPbK), 2 * kPrK);
+            tc::mbar_init(bar(kPbV), 2 * kPrV);
+            tc::mbar_init(bar(kPbP), 2 * kPrSoft);
             for (int i = 0; i < 2; i++) {
-                tc::mbar_init(bar(kPbSFree + i), 8);
+                tc::mbar_init(bar(kPbSFree + i), 2 * kPrSoft);
                 tc::mbar_init(bar(kPbS + i), 1);
                 tc::mbar_init(bar(kPbDone + i), 1);
             }
-            for (int i = 0; i < kPrMeta; i++) tc::mbar_init(bar(kPbMeta + i), 8);
+            for (int i = 0; i < kPrMeta; i++) tc::mbar_init(bar(kPbMeta + i), kPrK);
             tc::mbar_fence_init();
         }
     }
@@ -169,81 +173,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
     auto wait = [&](int i, int use) {
-        if (ok && !cluster_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
+        if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
     };
 
-    if (warp >= kPrWarpWiden && warp < kPrWarpMma) {
-        // ---------------- widening ----------------
-        constexpr int kKp = R::kPieces / 4;                   // pieces of K of a thread
-        constexpr int kVp = R::kPieces / 8;                   // pieces of V of a thread, in each of two rows
-        const int w = warp - kPrWarpWiden, jl = lane & 7, part4 = lane >> 3;
-        const int32_t *list = a.rows + static_cast<int64_t>(b) * a.width;
-        // the row of key 64 half + 8 w + jl of tile t, -1: none
-        auto row_of = [&](int t, int half) -> int64_t {
-            if (t >= t1) return -1;
-            const int k = half * 64 + w * 8 + jl;
-            if (t < prefix) {
-                const int j = t * kPrKeys + k;
-                const int r = j < plen ? __ldg(list + j) : -1;
-                return (r >= 0 && r < a.n_rows) ? r : -1;
-            }
-            return k < tree_n ? static_cast<int64_t>(b) * a.n_nodes + k : -1;
+    const int32_t *list = a.rows + static_cast<int64_t>(b) * a.width;
+    // the list's entry (or drafted row) of key `key` of tile t, and the row it means, -1: none. (An entry
+    // is looked at only when its row is needed: a test right behind the load would hold the warp.)
+    auto entry_of = [&](int t, int key) -> int {
+        if (t >= t1) return -1;
+        if (t >= prefix) return key < tree_n ? b * a.n_nodes + key : -1;
+        const int j = t * kPrKeys + key;
+        return j < plen ? __ldg(list + j) : -1;
+    };
+    auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
+    auto base_of = [&](int t) { return t < prefix ? a.cache : a.draft; };
+
+    if (warp >= kPrSoft && warp < kPrWarpV) {
+        // ---------------- K: keys 12 w .. 12 w + 11 of this CTA's half of each tile, whole rows ----------------
+        // Lanes 0-11 hold their rows, lanes 16-27 those of the same keys of the other half, for the scales.
+        constexpr int kN = kPrKn;
+        constexpr unsigned kAll = (1u << kN) - 1;
+        const int w = warp - kPrSoft, which = lane >> 4;
+        const bool holds = (lane & 15) < kN;
+        const int my_key = (which ? 1 - cta : cta) * kPrHalf + w * kN + (lane & 15);
+        unsigned char *codes = smem + L::kRawK + w * kN * R::kCodes;
+        unsigned char *tails = smem + L::kRawK + kPrHalf * R::kCodes + w * kN * R::kTail;
+        auto entry = [&](int t) { return holds ? entry_of(t, my_key) : -1; };
+        // the scale of a row of the other half (its own rows' scales come with them)
+        auto other_scale = [&](int t, int row) {
+            return which && row >= 0 ? __ldg(reinterpret_cast<const float *>(base_of(t) + static_cast<int64_t>(row) * R::kBytes +
+                                                                            R::kCodes + R::kSclAt))
+                                     : 0.0f;
         };
-        auto base_of = [&](int t) { return t < prefix ? a.cache : a.draft; };
-        // pieces of the own 256 dims: the row's piece of own piece m
-        auto own_piece = [&](int m) { return (m / (R::kPieces / 4)) * (R::kPieces / 2) + cta * (R::kPieces / 4) + m % (R::kPieces / 4); };
-        uint4 kv[kKp], vv[2][kVp];
-        uint32_t kes[R::kFp4 ? kKp : 1], ves[2][R::kFp4 ? kVp : 1];
-        float sc[2];
-        int64_t kr[2] = {-1, -1}, vr[2] = {-1, -1};                                 // rows of the tile held (K) and of V's, by half of the tile
-        auto load_k = [&](int t) {
-            const uint8_t *base = base_of(t);
-            const int64_t own = cta ? kr[1] : kr[0];
-#pragma unroll
-            for (int h = 0; h < 2; h++) sc[h] = R::scale(base, kr[h]);
-#pragma unroll
-            for (int i = 0; i < kKp; i++) {
-                kv[i] = R::codes(base, own, 4 * i + part4);
-                if constexpr (R::kFp4) kes[i] = R::block_scales(base, own, 4 * i + part4);
-            }
-        };
-        auto load_v = [&](int t) {
-            const uint8_t *base = base_of(t);
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int i = 0; i < kVp; i++) {
-                    const int k = own_piece(4 * i + part4);
-                    vv[h][i] = R::codes(base, vr[h], k);
-                    if constexpr (R::kFp4) ves[h][i] = R::block_scales(base, vr[h], k);
-                }
-        };
-        auto store_k = [&](int t) {
-            const int m = (t - t0) % kPrMeta;
+        int e1 = entry(t0 + 1);
+        int rows = row_of(t0, entry(t0));
+        R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
+        copy_commit();
+        float sc = other_scale(t0, rows);
+        for (int i = 0; i < n_tiles; i++) {
+            const int t = t0 + i, m = i % kPrMeta;
             const bool drafts = t >= prefix;
-            unsigned char *row = smem + L::kK + w * 8192 + jl * 16;
-#pragma unroll
-            for (int i = 0; i < kKp; i++)
-#pragma unroll
-                for (int u = 0; u < R::kLines; u++)
-                    *reinterpret_cast<uint4 *>(row + (R::kLines * (4 * i + part4) + u) * 128) =
-                        R::line(kv[i], R::kFp4 ? kes[R::kFp4 ? i : 0] : 0u, u, drafts);
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                // a drafted row with NaN codes: its scale makes every score with it NaN
-                if (kFmt != kFmtInt8 && drafts) {
-                    const unsigned nan = __ballot_sync(0xffffffffu, R::has_nan(a.draft, kr[h], part4));
-                    if ((nan >> jl) & 0x01010101u) sc[h] = __int_as_float(0x7fc00000);
+            const int e2 = entry(t + 2);
+            copy_wait<0>();
+            if (lane < kN) sc = R::scale(tails + lane * R::kTail);
+            if (kFmt != kFmtInt8 && drafts) {   // a drafted row with NaN codes: its scale makes every score with it NaN
+                unsigned bad = 0u;
+#pragma unroll 8
+                for (int r = 0; r < 32; r++) {
+                    const int row = __shfl_sync(0xffffffffu, rows, r);
+                    const uint8_t *p = a.draft + static_cast<int64_t>(max(row, 0)) * R::kBytes;
+                    if (row >= 0 && R::nan_share(p, p + R::kCodes)) bad |= 1u << r;
                 }
-                const unsigned valid = __ballot_sync(0xffffffffu, kr[h] >= 0) & 0xffu;
-                float mx = fabsf(sc[h]) < INFINITY ? sc[h] : 0.0f;
+                if (__reduce_or_sync(0xffffffffu, bad) >> lane & 1u) sc = __int_as_float(0x7fc00000);
+            }
+            if (kFmt != kFmtInt8 && drafts) R::clean(R::kFp4 ? tails : codes, kN * (R::kFp4 ? R::kTail : R::kCodes));
+            // (every read before the first write: the compiler keeps their order)
+            typename R::Line v[kN][2];                         // lines lane and lane + 32 of each row
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                if (lane < 8) scl[m * kPrKeys + h * 64 + w * 8 + lane] = sc[h];
-                if (lane == 0) {
-                    smx[m * 16 + h * 8 + w] = mx;
-                    val[m * 16 + h * 8 + w] = static_cast<uint8_t>(valid);
-                }
+            for (int r = 0; r < kN; r++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    v[r][h] = R::line(codes + r * R::kCodes, tails + r * R::kTail, lane + 32 * h, lane / 2 + 16 * h);
+            const unsigned bits = __ballot_sync(0xffffffffu, rows >= 0);
+            const float mx = finite_max(holds ? sc : 0.0f);
+            // the next rows, into the slots just read
+            const int nxt = row_of(t + 1, e1);
+            if (i + 1 < n_tiles) R::template fetch<kN>(codes, tails, base_of(t + 1), nxt, 0);
+            copy_commit();
+            const float sc_next = other_scale(t + 1, nxt);
+            if (i > 0) wait(kPbS + ((i - 1) & 1), (i - 1) >> 1);   // S(t - 1) is done: K is free
+            if (holds) {
+                scl[m * kPrKeys + my_key] = sc;
+                val[m * kPrKeys + my_key] = rows >= 0 ? 1 : 0;
+            }
+            if (lane == 0) {
+                smx[m * 8 + w] = mx;
+                full[m * 16 + cta * 8 + w] = (bits & kAll) == kAll ? 1 : 0;
+                full[m * 16 + (1 - cta) * 8 + w] = (bits >> 16 & kAll) == kAll ? 1 : 0;
+            }
+#pragma unroll
+            for (int r = 0; r < kN; r++) {
+                unsigned char *to = smem + L::kK + (lane >> 3) * L::kKBlock + swizzled(w * kN + r, lane & 7);
+#pragma unroll
+                for (int h = 0; h < 2; h++) *reinterpret_cast<uint4 *>(to + h * 4 * L::kKBlock) = R::widen(v[r][h]);
             }
             tc::fence_proxy_async();
             __syncwarp();
@@ -251,55 +263,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 tc::mbar_arrive(bar(kPbMeta + m));
                 arrive_leader(bar(kPbK));
             }
-        };
-        auto store_v = [&](int t) {
+            rows = nxt;
+            sc = sc_next;
+            e1 = e2;
+        }
+    } else if (warp >= kPrWarpV && warp < kPrWarpMma) {
+        // ---------------- V: keys 16 w .. 16 w + 15 of each tile, this CTA's 256 dims ----------------
+        constexpr int kN = kPrVn;
+        const int w = warp - kPrWarpV;
+        unsigned char *codes = smem + L::kRawV + w * kN * (R::kCodes / 2);
+        unsigned char *tails = smem + L::kRawV + kPrKeys * (R::kCodes / 2) + w * kN * R::kTail;   // (4-bit rows)
+        auto entry = [&](int t) { return lane < kN ? entry_of(t, w * kN + lane) : -1; };
+        const int block = (lane >> 4) * 16 + cta * 8 + (lane & 15) / 2;
+        int e1 = entry(t0 + 1);
+        R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
+        copy_commit();
+        for (int i = 0; i < n_tiles; i++) {
+            const int t = t0 + i;
             const bool drafts = t >= prefix;
+            const int e2 = entry(t + 2);
+            copy_wait<0>();
+            if (kFmt != kFmtInt8 && drafts) R::clean(R::kFp4 ? tails : codes, kN * (R::kFp4 ? R::kTail : R::kCodes / 2));
+            typename R::Line v[kN];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                unsigned char *row = smem + L::kV + (h * 8 + w) * 4096 + jl * 16;
+            for (int r = 0; r < kN; r++) v[r] = R::line(codes + r * (R::kCodes / 2), tails + r * R::kTail, lane, block);
+            const int nxt = row_of(t + 1, e1);
+            __syncwarp();
+            if (i + 1 < n_tiles) R::template fetch_half<kN>(codes, tails, base_of(t + 1), nxt, cta);
+            copy_commit();
+            if (i > 0) wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);   // O of t - 1 is done: V is free
+            unsigned char *to = smem + L::kV + (lane >> 3) * L::kVBlock;
 #pragma unroll
-                for (int i = 0; i < kVp; i++)
-#pragma unroll
-                    for (int u = 0; u < R::kLines; u++)
-                        *reinterpret_cast<uint4 *>(row + (R::kLines * (4 * i + part4) + u) * 128) =
-                            R::line(vv[h][i], R::kFp4 ? ves[h][R::kFp4 ? i : 0] : 0u, u, drafts);
-            }
+            for (int r = 0; r < kN; r++)
+                *reinterpret_cast<uint4 *>(to + swizzled(w * kN + r, lane & 7)) = R::widen(v[r]);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive_leader(bar(kPbV));
-        };
-        int64_t next[2];
-#pragma unroll
-        for (int h = 0; h < 2; h++) vr[h] = kr[h] = row_of(t0, h);
-        load_k(t0);
-        load_v(t0);
-#pragma unroll
-        for (int h = 0; h < 2; h++) next[h] = row_of(t0 + 1, h);
-        store_k(t0);
-        // rows of tile t + 1 (K) are taken over by V one step later
-#pragma unroll
-        for (int h = 0; h < 2; h++) kr[h] = next[h];
-        if (n_tiles > 1) load_k(t0 + 1);
-#pragma unroll
-        for (int h = 0; h < 2; h++) next[h] = row_of(t0 + 2, h);
-        for (int i = 0; i < n_tiles; i++) {
-            const int t = t0 + i;
-            if (i + 1 < n_tiles) {
-                wait(kPbS + (i & 1), i >> 1);                 // S(t) is done: K is free
-                store_k(t + 1);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; h++) vr[h] = kr[h];        // the rows of t + 1
-            if (i + 2 < n_tiles) {
-#pragma unroll
-                for (int h = 0; h < 2; h++) kr[h] = next[h];
-                load_k(t + 2);
-#pragma unroll
-                for (int h = 0; h < 2; h++) next[h] = row_of(t + 3, h);
-            }
-            if (i > 0) wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);   // O of t - 1 is done: V is free
-            store_v(t);
-            if (i + 1 < n_tiles) load_v(t + 1);
+            e1 = e2;
         }
     } else if (warp == kPrWarpMma) {
         // ---------------- tensor cores (the first CTA's, for both) ----------------
@@ -307,10 +307,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             constexpr uint32_t id_s = tc::idesc_f16(128, kPrKeys, false, false);
             constexpr uint32_t id_o = tc::idesc_f16(128, 256, false, true);
             const uint64_t dq = tc::desc(tc::smem_addr(smem + L::kQ), 128, 8192);
-            const uint64_t dk = tc::desc(tc::smem_addr(smem + L::kK), 128, 8192);
-            const uint64_t dv = tc::desc(tc::smem_addr(smem + L::kV), 4096, 128);
-            const uint64_t dp = tc::desc(tc::smem_addr(smem + L::kP), 128, 2048);
-            auto accumulate = [&](int i) {   // O += P(i) V(i): two products of 256 dims, K = 128 keys
+            const uint64_t dk = tc::desc_sw128(tc::smem_addr(smem + L::kK), 1024);
+            const uint64_t dv = tc::desc_sw128_mn(tc::smem_addr(smem + L::kV), L::kVBlock, 1024);
+            const uint64_t dp = tc::desc(tc::smem_addr(smem + L::kP), 128, L::kPGroup);
+            auto accumulate = [&](int i) {   // O += P(i) V(i): two products of 256 dims, K = 96 keys
                 wait(kPbV, i);
                 wait(kPbP, i);
                 ok = __all_sync(0xffffffffu, ok);
@@ -320,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                     for (int ks = 0; ks < kPrKeys / 16; ks++)
 #pragma unroll
                         for (int j = 0; j < 2; j++)
-                            mma_pair(tmem + j * 128, dp + ((ks * 256) >> 4), dv + ((ks * 2 * 4096 + j * 2048) >> 4), id_o,
+                            mma_pair(tmem + j * 128, dp + ((ks * 256) >> 4), dv + ((ks * 2048 + j * 2 * L::kVBlock) >> 4), id_o,
                                      (i > 0 || ks > 0) ? 1u : 0u);
                     commit_pair(bar(kPbDone + (i & 1)));
                 }
@@ -332,10 +332,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 if (i >= 2) wait(kPbSFree + (i & 1), (i >> 1) - 1);
                 ok = __all_sync(0xffffffffu, ok);
                 tc::fence_after_sync();
-                if (tc::elect_one()) {   // S(i) = Q K(i)^T: N = 128 keys, K = 512
+                if (tc::elect_one()) {   // S(i) = Q K(i)^T: N = 96 keys, K = 512
 #pragma unroll
                     for (int ks = 0; ks < kLatent / 16; ks++)
-                        mma_pair(tmem + kPrSCol + (i & 1) * 64, dq + ((ks * 256) >> 4), dk + ((ks * 256) >> 4), id_s,
+                        mma_pair(tmem + kPrSCol + (i & 1) * kPrSStep, dq + ((ks * 256) >> 4),
+                                 dk + (((ks >> 2) * L::kKBlock + (ks & 3) * 32) >> 4), id_s,
                                  ks > 0 ? 1u : 0u);
                     commit_pair(bar(kPbS + (i & 1)));
                 }
@@ -346,157 +347,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else {
         // ---------------- softmax ----------------
-        // the query rows as fp16 first: each warp two groups of 8 rows, four lanes a row
+        // the query rows as fp16 first: each warp two groups of 8 rows, four lanes a row, read twice (the
+        // second time from a cache) so that few of them are held
 #pragma unroll 1
-        for (int g = warp; g < kPrRows / 8; g += 4) {
+        for (int g = warp; g < kPrRows / 8; g += kPrSoft) {
             const int qr = g * 8 + (lane & 7);
             const bool real = r0 + qr < live;
             const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + (static_cast<int64_t>(b) * n_rows_q + (real ? r0 + qr : 0)) * kLatent);
-            uint4 v[16];
+                a.q + (static_cast<int64_t>(b) * n_rows_q + (real ? r0 + qr : 0)) * kLatent) + (lane >> 3);
             unsigned mx = 0u;
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                v[i] = real ? __ldg(src + 4 * i + (lane >> 3)) : make_uint4(0u, 0u, 0u, 0u);
-                mx = max(mx, bf16_absmax(v[i]));
-            }
+            for (int i = 0; i < 64; i += 4) mx = max(mx, real ? bf16_absmax(__ldg(src + i)) : 0u);
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const int e = query_exponent(mx);
-            const float f = pow2f_exact(e);
+            const float f = real ? pow2f_exact(e) : 0.0f;
             if (lane < 8) rowk[qr] = a.sm_scale * 1.4426950408889634f * pow2f_exact(-e);
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                *reinterpret_cast<uint4 *>(smem + L::kQ + g * 8192 + (4 * i + (lane >> 3)) * 128 + (lane & 7) * 16) =
-                    bf16_to_f16x8(v[i], f);
+            unsigned char *to = smem + L::kQ + g * 8192 + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll 4
+            for (int i = 0; i < 64; i += 4) *reinterpret_cast<uint4 *>(to + i * 128) = bf16_to_f16x8(__ldg(src + i), f);
         }
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive_leader(bar(kPbQ));
-        named_sync(1, 128);
+        named_sync(1, 32 * kPrSoft);
 
-        const int row = (warp & 1) * 32 + lane, half = warp >> 1;       // tensor-memory lane 32 warp + lane
+        // tensor-memory lane 32 warp + lane: row, and the lower or upper 48 keys of a tile
+        const int row = (warp & 1) * 32 + lane, half = warp >> 1, key0 = half * kPrHalf;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
         const int r = r0 + row;
         const float qk = rowk[row];
         const uint64_t seen = r < live ? a.mask[static_cast<int64_t>(b) * a.n_nodes + r / H] : 0ull;
         float ref = 0.0f, l = 0.0f, sigma = 0.0f;
         bool none = true;                                               // the row has seen no key
-        unsigned char *prow = smem + L::kP + (row >> 3) * 2048 + half * 1024 + (row & 7) * 16;
+        float *mine = red + half * 64 + row, *other = red + (1 - half) * 64 + row;   // two threads share a row
+        unsigned char *prow = smem + L::kP + (row >> 3) * L::kPGroup + key0 * 16 + (row & 7) * 16;
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
             wait(kPbMeta + m, i / kPrMeta);
             wait(kPbS + (i & 1), i >> 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
-            float x[64];
+            float x[kPrHalf];
+            const ulonglong2 *sc4 = reinterpret_cast<const ulonglong2 *>(scl + m * kPrKeys + key0);
             {
-                uint32_t s0[32], s1[32];
-                tc::tmem_ld32(tmem + lanes + kPrSCol + (i & 1) * 64, s0);
-                tc::tmem_ld32(tmem + lanes + kPrSCol + (i & 1) * 64 + 32, s1);
+                uint32_t s0[32], s1[16];
+                tc::tmem_ld32(tmem + lanes + kPrSCol + (i & 1) * kPrSStep, s0);
+                tc::tmem_ld16(tmem + lanes + kPrSCol + (i & 1) * kPrSStep + 32, s1);
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive_leader(bar(kPbSFree + (i & 1)));
-                const float4 *sc4 = reinterpret_cast<const float4 *>(scl + m * kPrKeys + half * 64);
+                const uint64_t qk2 = pack2(qk, qk), ref2 = pack2(-ref, -ref);
 #pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    const float4 s = sc4[e >> 2];
+                for (int e = 0; e < kPrHalf; e += 4) {
+                    const ulonglong2 s = sc4[e >> 2];
                     const uint32_t *v = e < 32 ? &s0[e] : &s1[e - 32];
-                    x[e] = fmaf(__uint_as_float(v[0]) * qk, s.x, -ref);
-                    x[e + 1] = fmaf(__uint_as_float(v[1]) * qk, s.y, -ref);
-                    x[e + 2] = fmaf(__uint_as_float(v[2]) * qk, s.z, -ref);
-                    x[e + 3] = fmaf(__uint_as_float(v[3]) * qk, s.w, -ref);
+                    unpack2(fma2(mul2(pack2(v[0], v[1]), qk2), s.x, ref2), x[e], x[e + 1]);
+                    unpack2(fma2(mul2(pack2(v[2], v[3]), qk2), s.y, ref2), x[e + 2], x[e + 3]);
                 }
             }
-            const uint2 vw = *reinterpret_cast<const uint2 *>(val + m * 16 + half * 8);
-            uint64_t keys = (static_cast<uint64_t>(vw.y) << 32) | vw.x;
-            if (t >= prefix) keys &= half == 0 ? seen : 0ull;        // what the node sees of the drafts
-            if (keys != ~0ull) {
+            const uint2 fw = *reinterpret_cast<const uint2 *>(full + m * 16 + half * 8);
+            const bool partial = (fw.x & fw.y) != 0x01010101u || t >= prefix;
+            uint64_t keys = (1ull << kPrHalf) - 1;                      // this thread's keys
+            if (partial) {
+                const uint2 *vb = reinterpret_cast<const uint2 *>(val + m * kPrKeys + key0);
+                keys = 0ull;
 #pragma unroll
-                for (int e = 0; e < 64; e++)
+                for (int g = 0; g < kPrHalf / 8; g++) {
+                    // eight bytes of 0 or 1 to eight bits
+                    const uint2 v = vb[g];
+                    keys |= static_cast<uint64_t>(((v.x * 0x10204080u) >> 28) | (((v.y * 0x10204080u) >> 28) << 4)) << (8 * g);
+                }
+                if (t >= prefix) keys &= seen >> key0;                  // what the node sees of the drafts
+#pragma unroll
+                for (int e = 0; e < kPrHalf; e++)
                     if (!((keys >> e) & 1ull)) x[e] = -INFINITY;
             }
             float mx = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 64; e++) mx = fmaxf(mx, x[e]);
-            const float4 *m4 = reinterpret_cast<const float4 *>(smx + m * 16);
-            float smax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float4 v = m4[e];
-                smax = fmaxf(smax, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-            }
+            for (int e = 0; e < kPrHalf; e += 2) mx = max3(mx, x[e], x[e + 1]);
+            const float4 ma = *reinterpret_cast<const float4 *>(smx + m * 8), mb = *reinterpret_cast<const float4 *>(smx + m * 8 + 4);
+            const float smax = fmaxf(max3(ma.x, ma.y, max3(ma.z, ma.w, mb.x)), max3(mb.y, mb.z, mb.w));
             const bool over = none ? mx > -INFINITY : mx > kGrow;
-            const bool grow = smax > 16.0f * sigma;                     // (sigma 0: no scale yet)
-            if (named_or(1, 128, over) || grow) {
+            const bool grow = smax > kSpread * sigma;                   // (sigma 0: no scale yet)
+            if (named_or(1, 32 * kPrSoft, over) || grow) {
                 // the references and sigma move; what they scale is rescaled
-                red[warp * 32 + lane] = mx;
+                *mine = mx;
                 const float sig_new = grow ? pow2_ceil(smax) : sigma;
                 const float beta = sigma == 0.0f ? 1.0f : sigma / sig_new;   // powers of two: exact
                 sigma = sig_new;
-                named_sync(1, 128);
-                const float mr = fmaxf(mx, red[(warp ^ 2) * 32 + lane]);
+                named_sync(1, 32 * kPrSoft);
+                const float mr = fmaxf(mx, *other);
                 const float delta = mr > (none ? -INFINITY : kGrow) ? mr : 0.0f;
                 const float alpha = none ? 0.0f : exp2f(-delta);
                 none = none && !(mr > -INFINITY);
                 ref += delta;
                 l *= alpha;
 #pragma unroll
-                for (int e = 0; e < 64; e++) x[e] -= delta;
+                for (int e = 0; e < kPrHalf; e++) x[e] -= delta;
                 if (i > 0) {
                     wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);
                     ok = __all_sync(0xffffffffu, ok);
                     tc::fence_after_sync();
                     const float f = alpha * beta;
+                    if (__any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 16) {
-                        uint32_t o[16];
-                        tc::tmem_ld16(tmem + lanes + c, o);
-                        tc::tmem_wait_ld();
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(tmem + lanes + c, o);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::tmem_st16(tmem + lanes + c, o);
+                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::tmem_st32(tmem + lanes + c, o);
+                        }
+                        tc::tmem_wait_st();
                     }
-                    tc::tmem_wait_st();
                     tc::fence_before_sync();
                 }
-                named_sync(1, 128);                                     // (red is free again)
+                named_sync(1, 32 * kPrSoft);                            // (red is free again)
             }
             const float inv = sigma > 0.0f ? kBoost / sigma : 1.0f;     // (sigma 0: every finite scale is 0)
-            uint32_t p[32];
-            const float4 *sc4 = reinterpret_cast<const float4 *>(scl + m * kPrKeys + half * 64);
+            uint32_t p[kPrHalf / 2];
+            const uint64_t inv2 = pack2(inv, inv);
+            uint64_t l2[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const float4 s = sc4[e >> 2];
-                const float p0 = exp2_approx(x[e]), p1 = exp2_approx(x[e + 1]), p2 = exp2_approx(x[e + 2]), p3 = exp2_approx(x[e + 3]);
-                l += (p0 + p1) + (p2 + p3);
-                p[e >> 1] = f16x2_rn(p0 * (s.x * inv), p1 * (s.y * inv));
-                p[(e >> 1) + 1] = f16x2_rn(p2 * (s.z * inv), p3 * (s.w * inv));
+            for (int e = 0; e < kPrHalf; e += 4) {
+                const ulonglong2 s = sc4[e >> 2];
+                const uint64_t p0 = pack2(exp2_approx(x[e]), exp2_approx(x[e + 1]));
+                const uint64_t p1 = pack2(exp2_approx(x[e + 2]), exp2_approx(x[e + 3]));
+                l2[0] = add2(l2[0], p0);
+                l2[1] = add2(l2[1], p1);
+                float y0, y1, y2, y3;
+                unpack2(mul2(p0, mul2(s.x, inv2)), y0, y1);
+                unpack2(mul2(p1, mul2(s.y, inv2)), y2, y3);
+                p[e >> 1] = f16x2_rn(y0, y1);
+                p[(e >> 1) + 1] = f16x2_rn(y2, y3);
             }
-            if (keys != ~0ull) {   // a key that is not one may have any scale: its weight is 0
+            {
+                float u0, u1;
+                unpack2(add2(l2[0], l2[1]), u0, u1);
+                l += u0 + u1;
+            }
+            if (partial) {   // a key that is not one may have any scale: its weight is 0
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
+                for (int e = 0; e < kPrHalf; e += 2) {
                     if (!((keys >> e) & 1ull)) p[e >> 1] &= 0xffff0000u;
                     if (!((keys >> (e + 1)) & 1ull)) p[e >> 1] &= 0x0000ffffu;
                 }
             }
             if (i > 0) wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);     // P(t - 1) has been read
 #pragma unroll
-            for (int g = 0; g < 8; g++)
+            for (int g = 0; g < kPrHalf / 8; g++)
                 *reinterpret_cast<uint4 *>(prow + g * 128) = make_uint4(p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]);
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive_leader(bar(kPbP));
         }
-        // the row's sum over both halves of the keys
-        red[warp * 32 + lane] = l;
-        named_sync(1, 128);
-        l += red[(warp ^ 2) * 32 + lane];
-        named_sync(1, 128);
+        // the row's sum over its two threads
+        *mine = l;
+        named_sync(1, 32 * kPrSoft);
+        l += *other;
+        named_sync(1, 32 * kPrSoft);
         const bool empty = r >= live || l == 0.0f;
         const float scale = sigma * (1.0f / kBoost);
-        if (half == 0) {
+        if (key0 == 0) {
             red[row] = empty ? 0.0f : (direct ? scale / l : scale);
             red[64 + row] = empty ? 0.0f : 1.0f;
             if (r < n_rows_q) {
@@ -516,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     const bool all_ok = __syncthreads_and(ok);
     if (!all_ok) {   // a wait gave up: the status word, and a bounded wait for products still in flight
         if (tid == 0) atomicOr(a.status, 64);
-        cluster_wait(bar(kPbDone + ((n_tiles - 1) & 1)), static_cast<uint32_t>(((n_tiles - 1) >> 1) & 1), kWaitLimit);
+        tc::mbar_wait(bar(kPbDone + ((n_tiles - 1) & 1)), static_cast<uint32_t>(((n_tiles - 1) >> 1) & 1), kWaitLimit);
         __syncthreads();
     }
     tc::fence_after_sync();
@@ -572,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
 template <int kFmt>
 cudaError_t launch_pair_t(const TreePlan &p, const TreeArgs &a, float *part_acc, float *part_ml, cudaStream_t stream) {
     auto kernel = tree_mla_pair_kernel<kFmt>;
-    const int smem = PrLayout::kBytes;
+    const int smem = PrLayout::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(2 * p.q_tiles, a.batch, p.parts), dim3(kPrThreads), smem, stream, a, p, part_acc,
