@@ -37,7 +37,7 @@ constexpr int kTrSoft = 8;                     // warps 0-7 softmax, then the wi
 constexpr int kTrKeys = 64;                    // keys of a tile
 constexpr float kTrNone = -1e30f;              // reference of a query row that has seen no key
 
-enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbQ = 10, kTbCount = 11 };
+enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbCount = 10 };
 
 template <int NQ>
 struct TrLayout {
@@ -47,9 +47,9 @@ struct TrLayout {
     static constexpr int kPBytes = kTrKeys * 2 * NQ;
     static constexpr int kPBufs = NQ == 64 ? 1 : 2;              // (what else shared memory holds of 64 rows)
     static constexpr int kP = kQ + NQ * 1024;                    // [kPBufs] P', core matrices of 8 keys x 8 query rows
-    static constexpr int kWiden = NQ == 64 ? 8 : 16;             // widening warps (64 rows: registers for their sums)
+    static constexpr int kWiden = 8;                              // widening warps
     static constexpr int kThreads = (kTrSoft + kWiden + 1) * 32;
-    static constexpr int kGroups = NQ == 16 ? 2 : 1;             // groups of 4 rows a widening warp has in flight
+    static constexpr int kGroups = NQ == 16 ? 4 : (NQ == 32 ? 2 : 1);            // groups of 4 rows a widening warp has in flight
     static constexpr int kRaw = kP + kPBufs * kPBytes;           // cache rows: codes, then tails, [kWiden warps][groups][4]
     static constexpr int kFac = kRaw + kWiden * kGroups * 4 * kRowBytes;                // [NQ] (score factor, reference) pairs
     static constexpr int kMask = kFac + NQ * 8;                  // [NQ] visibility words
@@ -106,28 +106,30 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     const uint32_t bar0 = tc::smem_addr(smem + L::kBar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
 
-    const int b = blockIdx.x, part = blockIdx.y, parts = plan.parts;
+    const int b = blockIdx.x / plan.q_tiles, r0 = (blockIdx.x - b * plan.q_tiles) * NQ, part = blockIdx.y, parts = plan.parts;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int H = a.n_heads;
-    const int n_rows_q = a.n_nodes * H;                       // query rows of the sequence (<= NQ)
+    const int n_rows_q = a.n_nodes * H;                       // query rows of the sequence; this CTA's: r0 .. r0 + NQ - 1
     const bool direct = parts == 1;
+    for (int i = tid; i < min(NQ, n_rows_q - r0) * 8; i += kThreads)   // (read when the lengths are there)
+        prefetch_line(a.q + (static_cast<int64_t>(b) * n_rows_q + r0) * kLatent + i * 64);
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
     const int plen = list_len(a, b), tree_n = tree_len(a, b);
     const int prefix = (plen + kTrKeys - 1) / kTrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
-    const int run = direct ? tiles : run_tiles(a, plan, kTrKeys);
+    const int run = direct ? tiles : run_tiles(a, plan, kTrKeys, tiles);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
-    const int live = tree_n * H;                              // query rows of the tree
+    const int live = tree_n * H - r0;                         // of this CTA's query rows, those of the tree
     const int n_tiles = live > 0 ? t1 - t0 : 0;
 
     // where each query row goes, and what it sees of the drafts
     if (tid < NQ) {
-        const int node = tid / H;
+        const int r = r0 + tid, node = r / H;
         int64_t o = -1;
-        if (tid < n_rows_q) {
-            o = static_cast<int64_t>(b) * n_rows_q + tid;
-            if (!direct) o = ((static_cast<int64_t>(b) * a.n_nodes + node) * parts + part) * H + (tid - node * H);
+        if (r < n_rows_q) {
+            o = static_cast<int64_t>(b) * n_rows_q + r;
+            if (!direct) o = ((static_cast<int64_t>(b) * a.n_nodes + node) * parts + part) * H + (r - node * H);
         }
         orow[tid] = o;
         mask[tid] = tid < live ? a.mask[static_cast<int64_t>(b) * a.n_nodes + node] : 0ull;
@@ -147,6 +149,74 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         if (tid < NQ && orow[tid] >= 0 && a.lse) a.lse[orow[tid]] = -INFINITY;
         return;
     }
+    // The warp's rows come into slots of its own in groups of four, each group refilled as soon as it
+    // is read; lanes 0 .. kN - 1 hold the entries of a tile's keys.
+    const bool widening = warp >= kTrSoft && warp < kTrWarpMma;
+    constexpr int kN = kTrKeys / L::kWiden, kGt = kN / 4, kG = L::kGroups;   // keys and groups of a tile
+    const int w = warp - kTrSoft;
+    unsigned char *codes = smem + L::kRaw + w * kG * 4 * R::kCodes;
+    unsigned char *tails = smem + L::kRaw + L::kWiden * kG * 4 * R::kCodes + w * kG * 4 * R::kTail;
+    const int32_t *list = a.rows + static_cast<int64_t>(b) * a.width;
+    // (An entry is looked at only when its row is needed: a test right behind the load would hold
+    // the warp until it is there.)
+    const int k = w * kN + lane;
+    auto entry_of = [&](int t) -> int {
+        if (t >= t1 || lane >= kN) return -1;
+        if (t >= prefix) return k < tree_n ? b * a.n_nodes + k : -1;
+        const int j = t * kTrKeys + k;
+        return j < plen ? __ldg(list + j) : -1;
+    };
+    auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
+    // starts copying group g (of four rows; kGt groups a tile, counted from the run's first); `rows`:
+    // what the lanes hold of its tile
+    auto request = [&](int g, int rows) {
+        if (g < kGt * n_tiles)
+            R::template fetch<4>(codes + g % kG * 4 * R::kCodes, tails + g % kG * 4 * R::kTail,
+                                 t0 + g / kGt < prefix ? a.cache : a.draft, rows, g % kGt * 4);
+        copy_commit();
+    };
+    // rows of tiles i .. i + 2, entries of the one after; the first copies go out before the barriers are there
+    int rows[3] = {-1, -1, -1}, entry = -1;
+    if (widening) {
+        int e[3];
+#pragma unroll
+        for (int u = 0; u < 3; u++) e[u] = entry_of(t0 + u);
+        entry = entry_of(t0 + 3);
+#pragma unroll
+        for (int u = 0; u < 3; u++) rows[u] = row_of(t0 + u, e[u]);
+#pragma unroll
+        for (int g = 0; g < kG; g++) request(g, rows[g / kGt]);
+    }
+    if (warp < kTrSoft) {
+        // the query rows as fp16, each scaled by the power of two that puts its largest magnitude in
+        // [2^14, 2^15): groups of 8 rows, the warps of a group and four lanes each sharing a row's pieces
+        constexpr int kGroups = NQ / 8;
+        constexpr int kStride = 32 / kGroups;                 // threads of a row
+        constexpr int kN = 64 / kStride;
+        const int qr = (warp % kGroups) * 8 + (lane & 7), p0 = (warp / kGroups) * 4 + (lane >> 3);
+        const bool real = qr < live;
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(b) * n_rows_q + r0 + (real ? qr : 0)) * kLatent);
+        named_sync(1, 256);                                   // (qmax is set)
+        uint4 v[kN];
+        unsigned mx = 0u;
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            v[i] = real ? __ldg(src + p0 + i * kStride) : make_uint4(0u, 0u, 0u, 0u);
+            mx = max(mx, bf16_absmax(v[i]));
+        }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        if (lane < 8) atomicMax(&qmax[qr], mx);
+        named_sync(1, 256);
+        const float f = pow2f_exact(query_exponent(qmax[qr]));
+        if (tid < NQ)
+            fac[tid] = make_float2(a.sm_scale * 1.4426950408889634f * pow2f_exact(-query_exponent(qmax[tid])), kTrNone);
+#pragma unroll
+        for (int i = 0; i < kN; i++)
+            *reinterpret_cast<uint4 *>(smem + L::kQ + (qr >> 3) * 8192 + (p0 + i * kStride) * 128 + (qr & 7) * 16) =
+                bf16_to_f16x8(v[i], f);
+        tc::fence_proxy_async();
+    }
     if (warp == kTrWarpMma) {
         tc::tmem_alloc(tc::smem_addr(tmem_slot), kCols);
         tc::tmem_relinquish();
@@ -159,7 +229,6 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tc::mbar_init(bar(kTbSFree + i), 8);
                 tc::mbar_init(bar(kTbP + i), 8);
             }
-            tc::mbar_init(bar(kTbQ), 8);
             tc::mbar_fence_init();
             *n_none = NQ;
         }
@@ -173,45 +242,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
     };
 
-    if (warp >= kTrSoft && warp < kTrWarpMma) {
+    if (widening) {
         // ---------------- widening: keys kN w .. kN w + kN - 1 of each tile ----------------
-        // The warp's rows come into slots of its own in groups of four, each group refilled as soon as it
-        // is read; lanes 0 .. kN - 1 hold the entries of a tile's keys.
-        constexpr int kN = kTrKeys / L::kWiden, kGt = kN / 4, kG = L::kGroups;   // keys and groups of a tile
-        const int w = warp - kTrSoft;
-        unsigned char *codes = smem + L::kRaw + w * kG * 4 * R::kCodes;
-        unsigned char *tails = smem + L::kRaw + L::kWiden * kG * 4 * R::kCodes + w * kG * 4 * R::kTail;
-        const int32_t *list = a.rows + static_cast<int64_t>(b) * a.width;
-        // (An entry is looked at only when its row is needed: a test right behind the load would hold
-        // the warp until it is there.)
-        const int k = w * kN + lane;
-        auto entry_of = [&](int t) -> int {
-            if (t >= t1 || lane >= kN) return -1;
-            if (t >= prefix) return k < tree_n ? b * a.n_nodes + k : -1;
-            const int j = t * kTrKeys + k;
-            return j < plen ? __ldg(list + j) : -1;
-        };
-        auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
-        // starts copying group g (of four rows; kGt groups a tile, counted from the run's first); `rows`:
-        // what the lanes hold of its tile
-        auto request = [&](int g, int rows) {
-            if (g < kGt * n_tiles)
-                R::template fetch<4>(codes + g % kG * 4 * R::kCodes, tails + g % kG * 4 * R::kTail,
-                                     t0 + g / kGt < prefix ? a.cache : a.draft, rows, g % kGt * 4);
-            copy_commit();
-        };
-        // rows of tiles i .. i + 2, entries of the one after
-        int rows[3], entry;
-        {
-            int e[3];
-#pragma unroll
-            for (int u = 0; u < 3; u++) e[u] = entry_of(t0 + u);
-            entry = entry_of(t0 + 3);
-#pragma unroll
-            for (int u = 0; u < 3; u++) rows[u] = row_of(t0 + u, e[u]);
-        }
-#pragma unroll
-        for (int g = 0; g < kG; g++) request(g, rows[g / kGt]);
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, buf = i & 1;
             const bool drafts = t >= prefix;
@@ -228,18 +260,23 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                         if (R::has_nan(first + r * R::kCodes, tail + r * R::kTail) && lane == h * 4 + r && valid) sc = __int_as_float(0x7fc00000);
                     R::clean(R::kFp4 ? tail : first, 4 * (R::kFp4 ? R::kTail : R::kCodes));
                 }
+                // the lines of the group, then the next group's copies into its slots, then the wait: what
+                // follows Done(i - 2) is on the path from it to S(i)
+                typename R::Line v[4][2];                     // lines lane and lane + 32 of each row
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++)
+                        v[r][u] = R::line(first + r * R::kCodes, tail + r * R::kTail, lane + 32 * u, lane / 2 + 16 * u);
+                __syncwarp();
+                request(g + kG, rows[(h + kG) / kGt]);
                 if (h == 0 && i >= 2) wait(kTbDone + buf, (i >> 1) - 1);   // C(i - 2) has been read
-#pragma unroll 2
+#pragma unroll
                 for (int r = 0; r < 4; r++) {
                     unsigned char *to = smem + L::kC + buf * L::kCBytes + (lane >> 3) * 8192 + swizzled(w * kN + h * 4 + r, lane & 7);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {              // lines lane and lane + 32
-                        const auto v = R::line(first + r * R::kCodes, tail + r * R::kTail, lane + 32 * u, lane / 2 + 16 * u);
-                        *reinterpret_cast<uint4 *>(to + u * 4 * 8192) = R::widen(v);
-                    }
+                    for (int u = 0; u < 2; u++) *reinterpret_cast<uint4 *>(to + u * 4 * 8192) = R::widen(v[r][u]);
                 }
-                __syncwarp();
-                request(g + kG, rows[(h + kG) / kGt]);
             }
             const float m = finite_max(sc);
             if (lane < kN) {
@@ -280,9 +317,15 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             }
             __syncwarp();
         };
-        wait(kTbQ, 0);
         for (int i = 0; i < n_tiles; i++) {
             const int buf = i & 1;
+            // whichever comes first, P(i - 1) or C(i): with two tiles in flight C(i) often waits for Done(i - 2)
+            bool early = false;
+            for (uint32_t k = 0; i > 0 && ok && k < kWaitLimit; k++) {
+                early = __all_sync(0xffffffffu, tc::mbar_test(bar(kTbP + (buf ^ 1)), ((i - 1) >> 1) & 1));
+                if (early || __all_sync(0xffffffffu, tc::mbar_test(bar(kTbFull + buf), (i >> 1) & 1))) break;
+            }
+            if (early) accumulate(i - 1);
             wait(kTbFull + buf, i >> 1);
             if (i >= 2) wait(kTbSFree + buf, (i >> 1) - 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -297,42 +340,11 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tc::mma_commit(bar(kTbS + buf));
             }
             __syncwarp();
-            if (i > 0) accumulate(i - 1);
+            if (i > 0 && !early) accumulate(i - 1);
         }
         accumulate(n_tiles - 1);
     } else {
         // ---------------- softmax ----------------
-        // the query rows as fp16, each scaled by the power of two that puts its largest magnitude in
-        // [2^14, 2^15): groups of 8 rows, the warps of a group and four lanes each sharing a row's pieces
-        {
-            constexpr int kGroups = NQ / 8;
-            constexpr int kStride = 32 / kGroups;                 // threads of a row
-            constexpr int kN = 64 / kStride;
-            const int qr = (warp % kGroups) * 8 + (lane & 7), p0 = (warp / kGroups) * 4 + (lane >> 3);
-            const bool real = qr < live;
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(b) * n_rows_q + (real ? qr : 0)) * kLatent);
-            uint4 v[kN];
-            unsigned mx = 0u;
-#pragma unroll
-            for (int i = 0; i < kN; i++) {
-                v[i] = real ? __ldg(src + p0 + i * kStride) : make_uint4(0u, 0u, 0u, 0u);
-                mx = max(mx, bf16_absmax(v[i]));
-            }
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if (lane < 8) atomicMax(&qmax[qr], mx);
-            named_sync(1, 256);
-            const float f = pow2f_exact(query_exponent(qmax[qr]));
-            if (tid < NQ)
-                fac[tid] = make_float2(a.sm_scale * 1.4426950408889634f * pow2f_exact(-query_exponent(qmax[tid])), kTrNone);
-#pragma unroll
-            for (int i = 0; i < kN; i++)
-                *reinterpret_cast<uint4 *>(smem + L::kQ + (qr >> 3) * 8192 + (p0 + i * kStride) * 128 + (qr & 7) * 16) =
-                    bf16_to_f16x8(v[i], f);
-            tc::fence_proxy_async();
-            named_sync(1, 256);
-            if (lane == 0) tc::mbar_arrive(bar(kTbQ));
-        }
         const int quad = warp & 3, hh = warp >> 2, c0 = hh * V;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const int j = quad * 16 + (lane & 15);                    // this thread's key of a tile (M = 64: lanes 0-15)
@@ -345,11 +357,17 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         for (int i = 0; i < n_tiles; i++) {
             const int buf = i & 1, t = t0 + i;
             wait(kTbFull + buf, i >> 1);                          // (the tile's scales and valid rows)
+            const bool key = lane < 16 && val[buf * kTrKeys + j] != 0;
+            const float sc = key ? scl[buf * kTrKeys + j] : 0.0f;
+            float smax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < L::kWiden / 4; e++) {
+                const float4 v = reinterpret_cast<const float4 *>(smx + buf * 16)[e];
+                smax = max3(smax, fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+            }
             wait(kTbS + buf, i >> 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
-            const bool key = lane < 16 && val[buf * kTrKeys + j] != 0;
-            const float sc = key ? scl[buf * kTrKeys + j] : 0.0f;
             // the scores of this thread's key less the references (0 for a row that has none)
             float x[V];
             {
@@ -370,12 +388,6 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
 #pragma unroll
                 for (int e = 0; e < V; e++)
                     if (!key || !((mask[c0 + e] >> j) & 1ull)) x[e] = -INFINITY;   // what each node sees of the drafts
-            }
-            float smax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < L::kWiden / 4; e++) {
-                const float4 v = reinterpret_cast<const float4 *>(smx + buf * 16)[e];
-                smax = max3(smax, fmaxf(v.x, v.y), fmaxf(v.z, v.w));
             }
             float top = -INFINITY;
 #pragma unroll
@@ -466,8 +478,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             const bool none = tid >= live || sum == 0.0f;         // (a node past the tree's, or no visible key)
             const float m = fac[tid].y * 0.6931471805599453f;
             const float scale = sigma * (1.0f / kBoost);
-            alpha[tid] = none ? 0.0f : (direct ? scale / sum : scale);
-            mask[tid] = none ? 0ull : 1ull;
+            alpha[tid] = none ? -1.0f : (direct ? scale / sum : scale);   // (-1: not a factor)
             if (orow[tid] >= 0) {
                 if (!direct) {
                     part_ml[2 * orow[tid]] = none ? -INFINITY : m;
@@ -487,28 +498,39 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     }
     tc::fence_after_sync();
     if (warp < 16) {
-        // O^T: tile mt of 128 latent dims, lane quadrant warp % 4 (dim 128 mt + 32 quad + lane)
+        // O^T: tile mt of 128 latent dims, lane quadrant warp % 4 (dim 128 mt + 32 quad + lane); rows of the
+        // output or partials in shared memory, over the C tiles, then one copy a row: stored from the
+        // registers, 4 bytes a lane, 64 rows took 6,300 cycles
         constexpr int CH = 16;
         const int mt = warp >> 2, dim = mt * 128 + (warp & 3) * 32 + lane;
         const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + mt * NQ;
 #pragma unroll 1
         for (int cb = 0; cb < NQ; cb += CH) {
+            float f[CH];                                      // (read before the first write: the compiler keeps the order)
+#pragma unroll
+            for (int e = 0; e < CH; e += 4) *reinterpret_cast<float4 *>(f + e) = *reinterpret_cast<const float4 *>(alpha + cb + e);
             uint32_t o[CH];
             tr_tmem_ld<CH>(ta + cb, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < CH; e++) {
-                const int64_t at = orow[cb + e];
-                const bool seen = mask[cb + e] != 0ull;
-                float v = seen ? __uint_as_float(o[e]) * alpha[cb + e] : 0.0f;
+                float v = f[e] == -1.0f ? 0.0f : __uint_as_float(o[e]) * f[e];
                 if (!all_ok) v = __int_as_float(0x7fc00000);
-                if (at >= 0) {
-                    if (direct) a.out[at * kLatent + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                    else if (seen) part_acc[at * kLatent + dim] = v;
-                }
+                if (direct) reinterpret_cast<uint16_t *>(smem + L::kC)[(cb + e) * kLatent + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                else reinterpret_cast<float *>(smem + L::kC)[(cb + e) * kLatent + dim] = v;
             }
         }
         if (!all_ok && direct && a.lse && tid < NQ && orow[tid] >= 0) a.lse[orow[tid]] = __int_as_float(0x7fc00000);
+    }
+    tc::fence_proxy_async();
+    __syncthreads();
+    if (lane == 0) {   // (a copy takes about 75 cycles to issue: every warp a few)
+        for (int r = warp; r < NQ; r += kThreads / 32) {
+            if (orow[r] < 0 || (!direct && alpha[r] == -1.0f)) continue;
+            if (direct) bulk_store(a.out + orow[r] * kLatent, smem + L::kC + r * kLatent * 2, kLatent * 2);
+            else bulk_store(part_acc + orow[r] * kLatent, smem + L::kC + r * kLatent * 4, kLatent * 4);
+        }
+        bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -524,7 +546,7 @@ cudaError_t launch_tree_t(const TreePlan &p, const TreeArgs &a, float *part_acc,
     const int smem = TrLayout<NQ>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, dim3(a.batch, p.parts), dim3(TrLayout<NQ>::kThreads), smem, stream, a, p, part_acc, part_ml);
+    e = launch_pdl(kernel, dim3(a.batch * p.q_tiles, p.parts), dim3(TrLayout<NQ>::kThreads), smem, stream, a, p, part_acc, part_ml);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -538,9 +560,12 @@ long long tree_tiles(long long width, int keys) { return (width + keys - 1) / ke
 TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms) {
     TreePlan p{};
     const int rows = n_nodes * n_heads;
-    const bool pair = rows > 64;
-    p.nq = rows <= 16 ? 16 : (rows <= 32 ? 32 : (pair ? 128 : 64));
-    p.q_tiles = pair ? (rows + 127) / 128 : 1;
+    // Few tiles: 16 query rows a CTA while each tile can have an SM of its own (64 rows over 67 keys:
+    // 22.5 us a call as one CTA a tile, 12.7 as four).
+    const bool small = static_cast<long long>(batch) * ((rows + 15) / 16) * tree_tiles(width, kTrKeys) <= num_sms;
+    const bool pair = rows > 64 && !small;
+    p.nq = rows <= 16 || small ? 16 : (rows <= 32 ? 32 : (pair ? 128 : 64));
+    p.q_tiles = (rows + p.nq - 1) / p.nq;
     p.units = pair ? num_sms / 2 : num_sms;
     const long long tiles = tree_tiles(width, pair ? kTreePairKeys : kTrKeys), base = static_cast<long long>(batch) * p.q_tiles;
     // one wave of runs when the lists are short (or there is one); else the kernel weighs up to four

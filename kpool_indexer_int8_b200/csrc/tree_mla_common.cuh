@@ -27,15 +27,15 @@ __device__ __forceinline__ int tile_count(const TreeArgs &a, int b, int keys) {
 // The tiles of a part: every sequence is cut into runs of as many, the length for which the busiest
 // of `units` SMs (or pairs) is done first, a run costing about six tiles more than its own (set-up,
 // output): up to `levels` waves of runs are tried, one when there is nothing to balance. Computed
-// by every warp for itself from the device's list lengths.
-__device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, int keys) {
+// by every warp for itself from the device's list lengths (own: the tiles of this CTA's sequence).
+__device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, int keys, int own) {
     const int lane = threadIdx.x & 31;
     auto reduce = [](int v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
-    const int first = lane < a.batch ? tile_count(a, lane, keys) : 0;
+    const int first = a.batch == 1 ? (lane == 0 ? own : 0) : (lane < a.batch ? tile_count(a, lane, keys) : 0);
     int sum = 0, most = 0;
     for (int s = lane; s < a.batch; s += 32) {
         const int n = s < 32 ? first : tile_count(a, s, keys);
@@ -71,6 +71,18 @@ __device__ __forceinline__ void copy16(void *to_smem, const void *from, bool the
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_addr(to_smem)), "l"(from), "r"(there ? 16 : 0)
                  : "memory");
 }
+// Copies `bytes` (a multiple of 16) of shared memory, written through the generic proxy before a proxy
+// fence and a barrier, to global memory; both 16-byte aligned. bulk_wait: the thread's
+// copies have read the shared memory (their writes are done when the kernel is).
+__device__ __forceinline__ void bulk_store(void *to, const void *from_smem, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(tc::smem_addr(from_smem)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// Asks for a line of 128 bytes ahead of its use.
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most kNewer of the groups committed last are still in flight; for the whole warp.
 template <int kNewer>

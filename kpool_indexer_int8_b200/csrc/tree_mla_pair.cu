@@ -34,7 +34,7 @@ constexpr int kPrMeta = 3;                     // tiles whose scales are kept
 constexpr uint32_t kPrSCol = 256;              // two score accumulators of 48 columns after the output's 256
 constexpr uint32_t kPrSStep = 64;
 
-enum PrBar { kPbQ = 0, kPbK, kPbV, kPbP, kPbSFree, kPbS = 6, kPbDone = 8, kPbMeta = 10, kPbCount = 13 };
+enum PrBar { kPbK = 0, kPbV, kPbP, kPbSFree, kPbS = 5, kPbDone = 7, kPbMeta = 9, kPbCount = 12 };
 
 struct PrLayout {
     static constexpr int kQ = 0;                                 // 8 row groups x 64 dim groups x 128 B
@@ -44,6 +44,7 @@ struct PrLayout {
     static constexpr int kV = kK + 8 * kKBlock;                  // 4 blocks of 64 own dims x 96 keys x 128 B, swizzled
     static constexpr int kPGroup = kPrKeys * 16;                 // 8 rows of P'
     static constexpr int kP = kV + 4 * kVBlock;                  // 8 row groups x 12 key groups x 128 B
+    static constexpr int kOutRow = kLatent * 2 + 16, kPartRow = kLatent * 4 + 16;   // rows of the epilogue
     static constexpr int kRawK = kP + 8 * kPGroup;               // the 48 own keys' rows: codes, then tails
     static constexpr int kRawV = kRawK + kPrHalf * kRowBytes;    // the own dims of 96 rows: codes, then tails of 4-bit rows
     static constexpr int kScl = kRawV + kPrKeys * 256;           // [3][96] row scales
@@ -58,7 +59,7 @@ struct PrLayout {
     static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
     static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 8 == 0 && kFull % 16 == 0 && kMax % 16 == 0 && kK % 1024 == 0 &&
                       kV % 1024 == 0 && kKBlock % 1024 == 0 && kVBlock % 1024 == 0 && kRawK % 128 == 0 && kRawV % 128 == 0, "alignment");
-    static_assert(kAlloc <= 232448, "shared memory of one CTA");
+    static_assert(kAlloc <= 232448 && kPrRows * kPartRow <= kP, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -115,10 +116,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     const int parts = plan.parts;
     const bool direct = parts == 1;
 
+    for (int i = tid; i < kPrRows * 8; i += kPrThreads)       // (read when the lengths are there)
+        if (r0 + (i >> 3) < n_rows_q) prefetch_line(a.q + (static_cast<int64_t>(b) * n_rows_q + r0) * kLatent + i * 64);
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
     const int plen = list_len(a, b), tree_n = tree_len(a, b);
     const int prefix = (plen + kPrKeys - 1) / kPrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
-    const int run = direct ? tiles : run_tiles(a, plan, kPrKeys);
+    const int run = direct ? tiles : run_tiles(a, plan, kPrKeys, tiles);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
     const int live = tree_n * H;                             // query rows of the tree
@@ -154,8 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc::fence_before_sync();
         if (lane == 0) {
-            tc::mbar_init(bar(kPbQ), 2 * kPrSoft);                      // (both CTAs' warps arrive at the first's)
-            tc::mbar_init(bar(kPbK), 2 * kPrK);
+            tc::mbar_init(bar(kPbK), 2 * kPrK);                         // (both CTAs' warps arrive at the first's)
             tc::mbar_init(bar(kPbV), 2 * kPrV);
             tc::mbar_init(bar(kPbP), 2 * kPrSoft);
             for (int i = 0; i < 2; i++) {
@@ -167,10 +169,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             tc::mbar_fence_init();
         }
     }
-    __syncthreads();
-    cluster_sync();
-    tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    // the barriers and tensor memory of both CTAs are there: every warp calls it once, after what its role
+    // can do before
+    uint32_t tmem;
+    auto start = [&]() {
+        named_sync(0, kPrThreads);
+        cluster_sync();
+        tc::fence_after_sync();
+        tmem = *tmem_slot;
+    };
     bool ok = true;
     auto wait = [&](int i, int use) {
         if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
@@ -210,6 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
         copy_commit();
         float sc = other_scale(t0, rows);
+        start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
             const bool drafts = t >= prefix;
@@ -278,6 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         int e1 = entry(t0 + 1);
         R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
         copy_commit();
+        start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i;
             const bool drafts = t >= prefix;
@@ -303,6 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else if (warp == kPrWarpMma) {
         // ---------------- tensor cores (the first CTA's, for both) ----------------
+        start();
         if (cta == 0) {
             constexpr uint32_t id_s = tc::idesc_f16(128, kPrKeys, false, false);
             constexpr uint32_t id_o = tc::idesc_f16(128, 256, false, true);
@@ -326,7 +336,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 }
                 __syncwarp();
             };
-            wait(kPbQ, 0);
             for (int i = 0; i < n_tiles; i++) {
                 wait(kPbK, i);
                 if (i >= 2) wait(kPbSFree + (i & 1), (i >> 1) - 1);
@@ -368,9 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             for (int i = 0; i < 64; i += 4) *reinterpret_cast<uint4 *>(to + i * 128) = bf16_to_f16x8(__ldg(src + i), f);
         }
         tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_leader(bar(kPbQ));
-        named_sync(1, 32 * kPrSoft);
+        start();
 
         // tensor-memory lane 32 warp + lane: row, and the lower or upper 48 keys of a tile
         const int row = (warp & 1) * 32 + lane, half = warp >> 1, key0 = half * kPrHalf;
@@ -535,6 +542,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         __syncthreads();
     }
     tc::fence_after_sync();
+    // the output or partials go through shared memory (over Q, K and V, which no product reads any more;
+    // rows 16 bytes apart in the banks), then one copy a row
+    const int stride = direct ? L::kOutRow : L::kPartRow;
     if (warp < 8) {
         // tensor-memory lane 32 (warp % 4) + lane: row, and the upper or lower 128 of the product's 256
         // dims; warps 0-3 the first product's dims, 4-7 the second's
@@ -542,12 +552,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         const int row = (quad & 1) * 32 + lane, r = r0 + row;
         const bool seen = red[64 + row] != 0.0f;
         const float f = red[row];
-        const bool put = r < n_rows_q && (direct || seen);
-        const int64_t o = put ? row_at(r) * kLatent + j * 256 + (quad >> 1) * 128 : 0;
+        const int dim0 = j * 256 + (quad >> 1) * 128;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
             uint32_t v[16];
-            __syncwarp();
             tc::tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + j * 128 + c, v);
             tc::tmem_wait_ld();
             float y[16];
@@ -556,7 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 y[e] = seen ? __uint_as_float(v[e]) * f : 0.0f;
                 if (!all_ok) y[e] = __int_as_float(0x7fc00000);
             }
-            if (put && direct) {
+            unsigned char *to = smem + row * stride + (dim0 + c) * (direct ? 2 : 4);
+            if (direct) {
 #pragma unroll
                 for (int g = 0; g < 2; g++) {
                     uint32_t w4[4];
@@ -565,15 +574,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                         const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[8 * g + 2 * e], y[8 * g + 2 * e + 1]);
                         w4[e] = *reinterpret_cast<const uint32_t *>(&h2);
                     }
-                    *reinterpret_cast<uint4 *>(a.out + o + c + 8 * g) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    *reinterpret_cast<uint4 *>(to + 16 * g) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
                 }
-            } else if (put) {
+            } else {
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(part_acc + o + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    *reinterpret_cast<float4 *>(to + 4 * e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
             }
         }
         if (!all_ok && direct && a.lse && j == 0 && quad < 2 && r < n_rows_q) a.lse[row_at(r)] = __int_as_float(0x7fc00000);
+    }
+    tc::fence_proxy_async();
+    __syncthreads();
+    if (lane == 0) {   // (a copy takes about 75 cycles to issue: every warp a few)
+        for (int row = warp; row < kPrRows; row += kPrThreads / 32) {
+            if (r0 + row >= n_rows_q || (!direct && red[64 + row] == 0.0f)) continue;
+            const int64_t o = row_at(r0 + row) * kLatent;
+            if (direct) bulk_store(a.out + o, smem + row * stride, kLatent * 2);
+            else bulk_store(part_acc + o, smem + row * stride, kLatent * 4);
+        }
+        bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();
