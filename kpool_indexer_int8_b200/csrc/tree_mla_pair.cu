@@ -116,8 +116,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     const int parts = plan.parts;
     const bool direct = parts == 1;
 
-    for (int i = tid; i < kPrRows * 8; i += kPrThreads)       // (read when the lengths are there)
-        if (r0 + (i >> 3) < n_rows_q) prefetch_line(a.q + (static_cast<int64_t>(b) * n_rows_q + r0) * kLatent + i * 64);
+    // the query rows as they are, where K and V will be (rows 16 bytes apart in the banks)
+#pragma unroll 1
+    for (int i = tid; i < kPrRows * 64; i += kPrThreads)
+        copy16(smem + L::kK + (i >> 6) * L::kOutRow + (i & 63) * 16,
+               a.q + (static_cast<int64_t>(b) * n_rows_q + min(r0 + (i >> 6), n_rows_q - 1)) * kLatent + (i & 63) * 8, true);
+    copy_commit();
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
     const int plen = list_len(a, b), tree_n = tree_len(a, b);
     const int prefix = (plen + kPrKeys - 1) / kPrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
@@ -133,6 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         return ((static_cast<int64_t>(b) * a.n_nodes + node) * parts + part) * H + (r - node * H);
     };
     if (n_tiles == 0) {   // no key for the pair, or no node of the tree
+        copy_wait<0>();
         if (direct)
             for (int i = tid; i < kPrRows * 64; i += kPrThreads) {
                 const int r = r0 + (i >> 6);
@@ -169,10 +174,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             tc::mbar_fence_init();
         }
     }
-    // the barriers and tensor memory of both CTAs are there: every warp calls it once, after what its role
-    // can do before
+    // Every warp calls it once, with its first cache rows requested: the query rows as fp16, each scaled by
+    // the power of two that puts its largest magnitude in [2^14, 2^15), by the first warps a group of 8
+    // each, a row by four lanes; then the barriers and tensor memory of both CTAs are there. (Rolled loops,
+    // from shared memory: held in registers and unrolled, it took 12,000 cycles of a first call's 48,000,
+    // for its instructions.)
     uint32_t tmem;
     auto start = [&]() {
+        named_sync(0, kPrThreads);
+        if (warp < kPrRows / 8) {
+            const int qr = warp * 8 + (lane & 7);
+            const bool real = r0 + qr < live;
+            const unsigned char *from = smem + L::kK + qr * L::kOutRow + (lane >> 3) * 16;
+            unsigned mx = 0u;
+#pragma unroll 4
+            for (int i = 0; i < 16; i++) mx = max(mx, bf16_absmax(*reinterpret_cast<const uint4 *>(from + 64 * i)));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const int e = query_exponent(mx);
+            const float f = pow2f_exact(e);
+            if (lane < 8) rowk[qr] = a.sm_scale * 1.4426950408889634f * pow2f_exact(-e);
+            unsigned char *to = smem + L::kQ + warp * 8192 + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll 2
+            for (int i = 0; i < 16; i++) {
+                const uint4 v = bf16_to_f16x8(*reinterpret_cast<const uint4 *>(from + 64 * i), f);
+                *reinterpret_cast<uint4 *>(to + 4 * i * 128) = real ? v : make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_proxy_async();
+        }
         named_sync(0, kPrThreads);
         cluster_sync();
         tc::fence_after_sync();
@@ -217,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
         copy_commit();
         float sc = other_scale(t0, rows);
+        copy_wait<1>();                                        // (the query rows)
         start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
@@ -286,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         int e1 = entry(t0 + 1);
         R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
         copy_commit();
+        copy_wait<1>();                                        // (the query rows)
         start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i;
@@ -312,6 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else if (warp == kPrWarpMma) {
         // ---------------- tensor cores (the first CTA's, for both) ----------------
+        copy_wait<0>();
         start();
         if (cta == 0) {
             constexpr uint32_t id_s = tc::idesc_f16(128, kPrKeys, false, false);
@@ -356,27 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else {
         // ---------------- softmax ----------------
-        // the query rows as fp16 first: each warp two groups of 8 rows, four lanes a row, read twice (the
-        // second time from a cache) so that few of them are held
-#pragma unroll 1
-        for (int g = warp; g < kPrRows / 8; g += kPrSoft) {
-            const int qr = g * 8 + (lane & 7);
-            const bool real = r0 + qr < live;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + (static_cast<int64_t>(b) * n_rows_q + (real ? r0 + qr : 0)) * kLatent) + (lane >> 3);
-            unsigned mx = 0u;
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) mx = max(mx, real ? bf16_absmax(__ldg(src + i)) : 0u);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const int e = query_exponent(mx);
-            const float f = real ? pow2f_exact(e) : 0.0f;
-            if (lane < 8) rowk[qr] = a.sm_scale * 1.4426950408889634f * pow2f_exact(-e);
-            unsigned char *to = smem + L::kQ + g * 8192 + (lane >> 3) * 128 + (lane & 7) * 16;
-#pragma unroll 4
-            for (int i = 0; i < 64; i += 4) *reinterpret_cast<uint4 *>(to + i * 128) = bf16_to_f16x8(__ldg(src + i), f);
-        }
-        tc::fence_proxy_async();
+        copy_wait<0>();
         start();
 
         // tensor-memory lane 32 warp + lane: row, and the lower or upper 48 keys of a tile
@@ -543,7 +555,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     }
     tc::fence_after_sync();
     // the output or partials go through shared memory (over Q, K and V, which no product reads any more;
-    // rows 16 bytes apart in the banks), then one copy a row
+    // rows 16 bytes apart in the banks), then, whole lines of them,
+    // to memory
     const int stride = direct ? L::kOutRow : L::kPartRow;
     if (warp < 8) {
         // tensor-memory lane 32 (warp % 4) + lane: row, and the upper or lower 128 of the product's 256
@@ -584,16 +597,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
         if (!all_ok && direct && a.lse && j == 0 && quad < 2 && r < n_rows_q) a.lse[row_at(r)] = __int_as_float(0x7fc00000);
     }
-    tc::fence_proxy_async();
     __syncthreads();
-    if (lane == 0) {   // (a copy takes about 75 cycles to issue: every warp a few)
-        for (int row = warp; row < kPrRows; row += kPrThreads / 32) {
-            if (r0 + row >= n_rows_q || (!direct && red[64 + row] == 0.0f)) continue;
-            const int64_t o = row_at(r0 + row) * kLatent;
-            if (direct) bulk_store(a.out + o, smem + row * stride, kLatent * 2);
-            else bulk_store(part_acc + o, smem + row * stride, kLatent * 4);
+    for (int row = warp; row < kPrRows; row += kPrThreads / 32) {
+        if (r0 + row >= n_rows_q || (!direct && red[64 + row] == 0.0f)) continue;
+        const uint4 *from = reinterpret_cast<const uint4 *>(smem + row * stride) + lane;
+        const int64_t o = row_at(r0 + row) * kLatent;
+        uint4 *to = (direct ? reinterpret_cast<uint4 *>(a.out + o) : reinterpret_cast<uint4 *>(part_acc + o)) + lane;
+        for (int c = 0; c < (direct ? 64 : 128); c += 64) {
+            const uint4 u = from[c], v = from[c + 32];
+            to[c] = u;
+            to[c + 32] = v;
         }
-        bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();
