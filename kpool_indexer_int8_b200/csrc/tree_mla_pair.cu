@@ -22,7 +22,7 @@ namespace {
 
 using namespace tree;
 
-constexpr int kPrSoft = 4, kPrK = 4, kPrV = 6; // warps 0-3 softmax, 4-7 K, 8-13 V, 14 tensor cores
+constexpr int kPrSoft = 4, kPrK = 6, kPrV = 4; // warps 0-3 softmax, 4-9 K, 10-13 V, 14 tensor cores
 constexpr int kPrWarpV = kPrSoft + kPrK, kPrWarpMma = kPrWarpV + kPrV;
 constexpr int kPrThreads = (kPrWarpMma + 1) * 32;
 constexpr int kPrRows = 64;                    // query rows of a CTA
@@ -48,7 +48,7 @@ struct PrLayout {
     static constexpr int kRawK = kP + 8 * kPGroup;               // the 48 own keys' rows: codes, then tails
     static constexpr int kRawV = kRawK + kPrHalf * kRowBytes;    // the own dims of 96 rows: codes, then tails of 4-bit rows
     static constexpr int kScl = kRawV + kPrKeys * 256;           // [3][96] row scales
-    static constexpr int kMax = kScl + kPrMeta * kPrKeys * 4;    // [3][8] largest finite scale of a K warp's keys (4 used)
+    static constexpr int kMax = kScl + kPrMeta * kPrKeys * 4;    // [3][8] largest finite scale of a K warp's keys (6 used)
     static constexpr int kValid = kMax + kPrMeta * 8 * 4;       // [3][96] bytes: 1 where there is a key
     static constexpr int kFull = kValid + kPrMeta * kPrKeys;     // [3][2][8] bytes: 1 where a K warp's keys are all there
     static constexpr int kRed = kFull + kPrMeta * 16;            // [2][64]
@@ -225,8 +225,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     auto base_of = [&](int t) { return t < prefix ? a.cache : a.draft; };
 
     if (warp >= kPrSoft && warp < kPrWarpV) {
-        // ---------------- K: keys 12 w .. 12 w + 11 of this CTA's half of each tile, whole rows ----------------
-        // Lanes 0-11 hold their rows, lanes 16-27 those of the same keys of the other half, for the scales.
+        // ---------------- K: keys 8 w .. 8 w + 7 of this CTA's half of each tile, whole rows ----------------
+        // Lanes 0-7 hold their rows, lanes 16-23 those of the same keys of the other half, for the scales.
         constexpr int kN = kPrKn;
         constexpr unsigned kAll = (1u << kN) - 1;
         const int w = warp - kPrSoft, which = lane >> 4;
@@ -306,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             e1 = e2;
         }
     } else if (warp >= kPrWarpV && warp < kPrWarpMma) {
-        // ---------------- V: keys 16 w .. 16 w + 15 of each tile, this CTA's 256 dims ----------------
+        // ---------------- V: keys 24 w .. 24 w + 23 of each tile, this CTA's 256 dims ----------------
         constexpr int kN = kPrVn;
         const int w = warp - kPrWarpV;
         unsigned char *codes = smem + L::kRawV + w * kN * (R::kCodes / 2);
