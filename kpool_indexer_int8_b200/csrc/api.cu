@@ -654,11 +654,8 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
     const glm::TreePlan plan = glm::tree_plan(batch, n_nodes, H, width, sms);
     rc = cuda_status(glm::launch_tree_mla(plan, a, format, part_acc, part_ml, st));
     if (rc != GLM_OK || plan.parts == 1) return rc;
-    // With fewer rows than SMs a row's partials go to four CTAs of four warps (16 rows of 148 partials:
-    // 20 us less a call than one CTA a row), else to one CTA (3,328 rows of 4: 26 us less, 512 of 18: 1.5).
-    if (batch * n_nodes * H < sms)
-        return cuda_status(glm::launch_mla_combine(part_acc, part_ml, batch * n_nodes, H, plan.parts, out, nullptr, lse, st));
-    return cuda_status(glm::launch_tree_combine(part_acc, part_ml, batch * n_nodes * H, H, plan.parts, a.out, lse, st));
+    return cuda_status(
+        glm::launch_tree_combine(part_acc, part_ml, batch * n_nodes * H, H, plan.parts, sms, a.out, lse, st));
 }
 }  // namespace
 

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             }
             const float m = finite_max(sc);
             if (lane < kN) {
-                scl[buf * kTrKeys + k] = sc;
+                scl[buf * kTrKeys + k] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
                 val[buf * kTrKeys + k] = valid ? 1 : 0;
             }
             if (lane == 0) smx[buf * 16 + w] = m;
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         if (tid < NQ) {
             const float sum = (red[tid] + red[NQ + tid]) + (red[2 * NQ + tid] + red[3 * NQ + tid]);
             const bool none = tid >= live || sum == 0.0f;         // (a node past the tree's, or no visible key)
-            const float m = fac[tid].y * 0.6931471805599453f;
+            // (scores that are all NaN set no reference: theirs is 0)
+            const float m = fac[tid].y == kTrNone ? 0.0f : fac[tid].y * 0.6931471805599453f;
             const float scale = sigma * (1.0f / kBoost);
             alpha[tid] = none ? -1.0f : (direct ? scale / sum : scale);   // (-1: not a factor)
             if (orow[tid] >= 0) {

@@ -41,8 +41,8 @@ cudaError_t launch_tree_mla(const TreePlan &plan, const TreeArgs &a, int format,
                             cudaStream_t stream);
 
 // Merges the `parts` partials of each of n_rows = batch * n_nodes * n_heads query rows.
-cudaError_t launch_tree_combine(const float *part_acc, const float *part_ml, int n_rows, int n_heads, int parts, uint16_t *out,
-                                float *lse, cudaStream_t stream);
+cudaError_t launch_tree_combine(const float *part_acc, const float *part_ml, int n_rows, int n_heads, int parts, int num_sms,
+                                uint16_t *out, float *lse, cudaStream_t stream);
 cudaError_t launch_tree_pair(const TreePlan &plan, const TreeArgs &a, int format, float *part_acc, float *part_ml,
                              cudaStream_t stream);
 

@@ -281,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             const float sc_next = other_scale(t + 1, nxt);
             if (i > 0) wait(kPbS + ((i - 1) & 1), (i - 1) >> 1);   // S(t - 1) is done: K is free
             if (holds) {
-                scl[m * kPrKeys + my_key] = sc;
+                scl[m * kPrKeys + my_key] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
                 val[m * kPrKeys + my_key] = rows >= 0 ? 1 : 0;
             }
             if (lane == 0) {
