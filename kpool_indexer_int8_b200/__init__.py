@@ -16,8 +16,11 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libglm_dsa.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python kpool_indexer_int8_b200/build.py`")
+for _built in (LIB_PATH, os.path.join(_HERE, "_args.so")):
+    if not os.path.exists(_built):
+        raise ImportError(f"{_built} is missing: build it with `python kpool_indexer_int8_b200/build.py`")
+
+from . import _args                                        # noqa: E402  (the built checks of csrc/args.c)
 
 lib = C.CDLL(LIB_PATH)
 
@@ -559,6 +562,8 @@ lib.glm_tree_commit.argtypes = [_D, _P, _I32, _P, _I32, _I32, _I64, _P, _P, _P, 
 lib.glm_tree_commit.restype = C.c_int
 
 
+_args.setup(torch.Tensor, [(torch.int8, 0, 8), (torch.int32, 0, 32), (torch.int64, 0, 64), (torch.uint8, 1, 8),
+                           (torch.float32, 2, 32), (torch.bfloat16, 4, 16)])   # DLPack: 0 int, 1 uint, 2 float, 4 bfloat
 _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -577,18 +582,18 @@ def _bad(t, dtype, shape, name, device):
 
 def _take(device, *named):
     """Addresses of the tensors of a call, checked: (tensor or None, dtype, shape or None, name) each, all
-    contiguous on one device. (One pass with few Python calls: the checks of a decode step's calls are
-    on its critical path. get_device() is -1 for a tensor of the CPU.)"""
-    out = []
-    for t, dtype, shape, name in named:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != device or t.dtype is not dtype or not t.is_contiguous() or \
-                (shape is not None and t.shape != shape):
-            raise _bad(t, dtype, shape or t.shape, name, device)
-        out.append(t.data_ptr())
-    return out
+    contiguous on one device. The checks of a decode step's calls are on its critical path, so they are
+    native; a tensor that fails them (or that the native code cannot see) is looked at again here."""
+    return _args.take(device, *named) or [_address(device, *n) for n in named]
+
+
+def _address(device, t, dtype, shape, name):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        raise _bad(t, dtype, shape or t.shape, name, device)
+    return t.data_ptr()
 
 
 def _call(fn, name, device, stream, *args):

@@ -4,6 +4,8 @@
 
 Each csrc/*.cu is compiled to an object under _build/ (rebuilt when it or a header changed) and
 linked into kpool_indexer_int8_b200/libglm_dsa.so with the CUDA runtime linked statically.
+csrc/args.c, the binding's checks of tensors, becomes kpool_indexer_int8_b200/_args.so (gcc, the headers
+of this Python and the DLPack header that torch ships).
 No fast-math: the int8 quantisation relies on IEEE fp32 division and round-half-to-even.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libglm_dsa.so")
+ARGS_SRC, ARGS_LIB = os.path.join(CSRC, "args.c"), os.path.join(PKG, "_args.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -44,8 +48,22 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_args(force: bool = False) -> str:
+    if force or not os.path.exists(ARGS_LIB) or os.path.getmtime(ARGS_LIB) < os.path.getmtime(ARGS_SRC):
+        import importlib.util
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(torch, "include"), ARGS_SRC, "-o", ARGS_LIB + ".tmp"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on {ARGS_SRC}:\n{r.stdout}\n{r.stderr}")
+        os.replace(ARGS_LIB + ".tmp", ARGS_LIB)
+    return ARGS_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_args(force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hm = _headers_mtime()
     todo = []

@@ -219,8 +219,9 @@ cudaError_t launch_block_tables(const BlockTableArgs &a, cudaStream_t stream, in
     ctas = std::max(ctas, (static_cast<int64_t>(a.batch) + kBtWarps - 1) / kBtWarps);
     ctas = std::min(std::max(ctas, static_cast<int64_t>(1)), static_cast<int64_t>(num_sms));
     const int smem = (4 * a.batch + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kBtMaxBatch + 1) * 4);
+    cudaError_t e = cudaSuccess;
+    if (smem > 47 * 1024)                       // (48 KB, less its own, need no asking)
+        e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * kBtMaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
     e = launch_pdl(block_tables_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kBtThreads), smem, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
