@@ -3,28 +3,36 @@
 // drafted rows whose bit is set in its mask,
 //     s = sm_scale q . c,   out = sum softmax(s) c,   lse = log sum exp(s),   c = code * scale,
 // the latent row being key and value. Every (node, head) of a sequence is a row of one query
-// matrix, so that a widened tile of keys serves all of them. This file: at most 64 query rows;
-// tree_mla_pair.cu: more.
+// matrix, so that a widened tile of keys serves all of them. This file: tiles of at most 64 query rows;
+// tree_mla_pair.cu: of 128.
 //
-// One CTA per (sequence, run of its keys) walks its run 64 keys at a time, the drafted rows being
-// the last tile. Keys are the MMA M dimension, the NQ query rows the N dimension (as in the sparse
-// attention); 17 warps in three roles:
-//   * warps 8-15 (widening): each thread holds the pieces of one key row of the next two tiles in
-//     registers while the tile before is worked on, then writes them as fp16 (exact: int8 and E4M3
-//     codes, E2M1 code times block scale) to one of two tiles C[64 x 512] of 8x8 core matrices;
-//   * warp 16 (tensor cores): S^T(t) = C(t) . Q^T into one of two accumulators, then O^T += C(t-1)^T
-//     P(t-1)^T, so that the next scores are computed while the softmax of the tile before runs;
-//   * warps 0-7 (softmax): x = S scale_row qk - ref in log2 units, P' = 2^x scale_row / sigma as fp16.
-//     The reference of a query row moves only when a score passes it by 2^8 (a vote of the eight
-//     warps per tile), and sigma, a power of two, only when a row scale passes 16 sigma: then the
+// One CTA per (sequence, tile of query rows, run of keys) walks its run 64 keys at a time, the drafted
+// rows being the last tile. Keys are the MMA M dimension, the NQ query rows the N dimension (as in the
+// sparse attention); 17 warps in three roles:
+//   * warps 8-15 (widening): eight rows of each tile each. Rows come into slots of the warp's own by
+//     asynchronous copies, four at a time and (16 query rows) two tiles ahead, and are written as fp16
+//     (exact: int8 and E4M3 codes, E2M1 code times block scale) to one of two tiles C[64 x 512], rows of
+//     128 bytes in the 128-byte swizzle, which the tensor cores read both as keys and, transposed, as values;
+//   * warp 16 (tensor cores): S^T(t) = C(t) . Q^T into one of two accumulators, O^T += C(t)^T P(t)^T,
+//     whichever is ready first;
+//   * warps 0-7 (softmax): x = S scale_row qk - ref in log2 units, P' = 2^x scale_row 4 / sigma as fp16.
+//     The reference of a query row moves only when a score passes it by 2^12 (a vote of the eight
+//     warps per tile), and sigma, a power of two, only when a row scale passes 2 sigma: then the
 //     accumulator in tensor memory is rescaled, otherwise no maximum is taken. Sums stay in
 //     registers, one per thread and query row, until the end.
-// P' is one fp16 term: a weight is off by at most 2^-11 of itself (an eighth of the bf16 output's
-// 2^-8), or by 2^-28 of the largest once it is below 2^-17 of it.
+// P' <= 2^15 is one fp16 term: a weight is off by at most 2^-11 of itself (an eighth of the bf16
+// output's 2^-8), or by 2^-25 sigma / 4 once P' is below 2^-14.
 //
-// A sequence's keys are cut into runs so that the CTAs fill the SMs; the combine kernel of the
-// sparse attention merges the partials. Every wait is bounded; one that gives up sets the status
-// word and the CTA writes NaN.
+// A sequence's keys are cut into runs so that the CTAs fill the SMs; tree_combine.cu merges the
+// partials. Every wait is bounded; one that gives up sets the status word and the CTA writes NaN.
+//
+// What bounds it: with 16 query rows and a long list, the chain from a free C tile through widening
+// (about 700 cycles), S (32 products of 23, 1,100 with their latency), softmax (1,700) and O (900), of which
+// two are in flight: a 64-key tile takes 3,300 cycles, where shared memory (C written once and read twice)
+// would allow 2,000. 262,144 4-bit rows, 16 query rows: 73 us a call with the merge, 1.1 TB/s; the rows at
+// the copy rate would take 12. A small call is bound by its start and end and, cold, by its
+// instructions: 67 int8 keys and 64 query rows take 11.4 us of the GPU, merge
+// included.
 #include "tree_mla_common.cuh"
 
 namespace glm {

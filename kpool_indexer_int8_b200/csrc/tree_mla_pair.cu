@@ -1,19 +1,29 @@
 // tree_mla_pair.cu -- the tree attention for more than 64 query rows (node, head) of a sequence:
-// two CTAs of a cluster work on 128 query rows and 128 keys at a time with paired tensor-core
+// two CTAs of a cluster work on 128 query rows and 96 keys at a time with paired tensor-core
 // instructions (cta_group::2, M = 128), which hold 64 rows x 512 outputs in half of each CTA's
 // tensor memory and let each CTA keep only its half of every B operand:
-//     S = Q K^T     A: this CTA's 64 rows of Q       B: K, this CTA's 64 keys x 512 dims
-//     O += P V      A: this CTA's 64 rows of P       B: V, 128 keys x this CTA's 256 dims
-// A key tile is thus widened one and a half times (K and V copies of its own quarter) for 128 query rows, where the
-// one-CTA kernel (tree_mla.cu) widens it once for 64 and reads its operands from shared memory
-// twice as often; shared-memory bandwidth is what bounds both. Roles of the 13 warps of a CTA:
-//   * warps 4-11 (widening): K(t + 1) once S(t) is done, V(t) once O of t - 1 is done; the codes of
-//     the tile after are in registers meanwhile;
-//   * warp 12 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs;
+//     S = Q K^T     A: this CTA's 64 rows of Q       B: K, this CTA's 48 keys x 512 dims
+//     O += P V      A: this CTA's 64 rows of P       B: V, 96 keys x this CTA's 256 dims
+// A key tile is thus widened twice over the pair (as K and as V) for 128 query rows, where the one-CTA
+// kernel (tree_mla.cu) widens it once for 64 and reads its operands from shared memory twice as
+// often. Roles of the 15 warps of a CTA, each with its own raw rows in shared memory, filled by
+// asynchronous copies a tile ahead:
 //   * warps 0-3 (softmax): one thread per row and half of the keys (tensor-memory lane = row, the
-//     upper 64 lanes hold the tile's upper 64 keys): references, sums and P' as in tree_mla.cu, the
-//     two halves of a row meeting only when a reference moves.
-// K and V have one buffer each: while S(t + 1) runs V(t) is written, while O of t runs K(t + 2).
+//     upper 64 lanes hold the tile's upper 48 keys): references, sums and P' as in tree_mla.cu, the
+//     two halves of a row meeting only when a reference moves;
+//   * warps 4-9 (K): whole rows of the CTA's 48 keys as fp16 once S(t - 1) is done, and the scales of all 96;
+//   * warps 10-13 (V): the CTA's 256 dims of the 96 keys once O of t - 1 is done;
+//   * warp 14 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs.
+// K, V and P have one buffer each: shared memory holds no more beside Q.
+//
+// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,680 cycles of a CTA: 2,230 cycles of
+// shared-memory wavefronts of the warps (counted; rows copied in and read, 49 KB each way, K and V 48 KB each
+// and P 12 KB written, scales, barriers) and 184 KB of operands read by the tensor cores (Q 64, K 48, V
+// 48, P twice 12), 1,470 cycles: 3,700. Tensor pipe 42 % active, issue 46 %. 8 nodes of 64 heads over
+// 262,144 int8 rows: 380 us a call, 720 TFLOP/s (350 us and 780 alone on a cool chip), 0.44 of the
+// measured bf16 rate. What was tried on top of it and did not pay: two teams of softmax warps on alternate
+// tiles (410 us), eight softmax warps on one tile (386), rows read in rolled loops right before they are
+// widened (390-404), one set of warps for K and V (391).
 #include "tree_mla_common.cuh"
 
 namespace glm {
