@@ -421,9 +421,10 @@ int glm_mla_v_up(const glm_dsa_dims *dims, const void *o_lat_dev, const void *w_
  *   workspace_dev / ws_bytes: >= glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width),
  *               256-byte aligned. Its last 256 bytes start with a status word set nonzero if a wait
  *               on the tensor cores gave up (outputs then invalid; never cleared by the library).
- * 1 <= n_nodes <= 64, 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with
+ *               Calls that may run at the same time (other streams, graphs) need workspaces of their own.
+ * out must not overlap q (refused) nor any other input. 1 <= n_nodes <= 64, 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with
  * mask 1 is an ordinary decode token whose own row is not in the cache yet. A row that a node does
- * not see has no effect on it, whatever it holds. The products run on the tensor cores with fp16
+ * not see has no effect on it, whatever it holds; a NaN or an infinite scale that it sees makes it NaN. The products run on the tensor cores with fp16
  * operands and fp32 accumulation: codes and (scaled by powers of two) queries exactly, the softmax
  * weights times the row scale rounded to fp16 (2^-11 relative), sums and references in fp32.
  */

@@ -627,6 +627,8 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
         (lse && !aligned(lse, 4)))
         return GLM_ERR_INVALID_ARG;
     const int H = dims->n_heads, sms = num_sms();
+    const size_t q_bytes = static_cast<size_t>(batch) * n_nodes * H * glm::kLatent * 2;
+    if (overlap(q, q_bytes, out, q_bytes)) return GLM_ERR_INVALID_ARG;   // (CTAs read q while others write out)
     const size_t need = glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width);
     if (workspace == nullptr || ws_bytes < need || !aligned(workspace, 256)) return GLM_ERR_WORKSPACE;
     const size_t partials = glm::tree_partials(batch, n_nodes, H, width, sms);
@@ -635,7 +637,7 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
     float *part_ml = reinterpret_cast<float *>(ws + mla_acc_bytes(partials));
     glm::TreeArgs a{};
     a.q = static_cast<const uint16_t *>(q);
-    a.cache = static_cast<const uint8_t *>(cache);
+    a.cache = static_cast<const uint8_t *>(cache ? cache : draft);   // (no row: an address of nothing that is read)
     a.n_rows = n_rows;
     a.rows = rows;
     a.row_len = row_len;

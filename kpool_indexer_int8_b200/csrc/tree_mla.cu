@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
                     const float4 f = f4[e >> 1];
-                    x[e] = fmaf(__uint_as_float(r[e]) * sc, f.x, f.y == kTrNone ? 0.0f : -f.y);
-                    x[e + 1] = fmaf(__uint_as_float(r[e + 1]) * sc, f.z, f.w == kTrNone ? 0.0f : -f.w);
+                    x[e] = fmaf(__uint_as_float(r[e]) * f.x, sc, f.y == kTrNone ? 0.0f : -f.y);
+                    x[e + 1] = fmaf(__uint_as_float(r[e + 1]) * f.z, sc, f.w == kTrNone ? 0.0f : -f.w);
                 }
             }
             if (!key || t >= prefix) {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 for (int e = 0; e < V; e++) m[e] = x[e];
                 const float bm = butterfly<V, true>(m);
                 if ((lane & kLow) == 0) red[quad * NQ + c0 + ((lane >> kShift) & (V - 1))] = bm;
-                const float sig_new = grow ? pow2_ceil(smax) : sigma;
+                const float sig_new = grow ? sigma_of(smax) : sigma;
                 const float beta = sigma == 0.0f ? 1.0f : sigma / sig_new;   // powers of two: exact
                 sigma = sig_new;
                 if (tid == 0) *n_none = 0;

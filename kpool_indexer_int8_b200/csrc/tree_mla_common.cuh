@@ -273,6 +273,8 @@ __device__ __forceinline__ float finite_max(float v) {
 }
 // The power of two that puts a bf16 magnitude (its bits) in [2^14, 2^15): bf16 values so scaled are
 // exact in fp16 (those below 2^-17 of the range aside).
+// sigma for a largest scale: the power of two at or above it, and such that kBoost / sigma is finite.
+__device__ __forceinline__ float sigma_of(float smax) { return fmaxf(pow2_ceil(smax), 0x1p-125f); }
 __device__ __forceinline__ int query_exponent(unsigned bits) {
     return bits == 0u ? 0 : min(120, max(-120, 14 - (static_cast<int>(bits >> 7) - 127)));
 }

@@ -463,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             if (named_or(1, 32 * kPrSoft, over) || grow) {
                 // the references and sigma move; what they scale is rescaled
                 *mine = mx;
-                const float sig_new = grow ? pow2_ceil(smax) : sigma;
+                const float sig_new = grow ? sigma_of(smax) : sigma;
                 const float beta = sigma == 0.0f ? 1.0f : sigma / sig_new;   // powers of two: exact
                 sigma = sig_new;
                 named_sync(1, 32 * kPrSoft);

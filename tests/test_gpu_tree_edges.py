@@ -265,3 +265,94 @@ def test_binding_refuses(cuda):
     CALL["int8"](dims, **good)
     torch.cuda.synchronize()
     check(c, good["out"], good["lse"])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("H", [4, 40])
+@pytest.mark.parametrize("top", [2.0 ** -126, 2.0 ** -140, 2.0 ** 100])
+def test_scales_at_the_ends_of_fp32(cuda, fmt, H, top):
+    # denormal scales lose bits as such (the rows are what they are), not in the sums
+    rng = np.random.default_rng(H)
+    c = case(rng, fmt, 1, 2, H, 200, [200], [2], n_rows=200)
+    for name in ("cache", "draft"):
+        n = len(c[name])
+        set_scale(c[name], np.arange(n), fmt, (top * rng.uniform(0.25, 1.0, n)).astype(np.float32))
+    sm = float(np.float32(2.0 ** -110 if top > 1 else SM))
+    out, lse = launch(c, cuda, sm=sm)
+    o = out.float().cpu().numpy().astype(np.float64)
+    q = synth.bf16_bits_to_f32(c["q"]).astype(np.float64)
+    for b, i, want, wl, tol, ltol in R.tree(q, c["cache"], c["rows"], c["row_len"], c["draft"], c["masks"], c["n_tree"], sm, fmt):
+        # (a bf16 or fp32 denormal is off by half its step more)
+        assert (np.abs(o[b, i] - want) <= tol + 2.0 ** -134 + 2.0 ** -148).all(), (b, i)
+        assert (np.abs(lse[b, i].cpu().numpy() - wl) <= ltol).all(), (b, i)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("H", [4, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_stays_alone(cuda, fmt, H, value):
+    rng = np.random.default_rng(8)
+    c = case(rng, fmt, 2, 3, H, 300, [300, 200], [3, 3], n_rows=400)
+    good = launch(c, cuda)
+    q = bf16(c["q"]).clone()
+    q[0, 1, H - 1, 77] = value
+    bad = dict(c, q=q.view(torch.int16).numpy().view(np.uint16))
+    out, lse = launch(bad, cuda)
+    assert torch.isnan(out[0, 1, H - 1]).all() and torch.isnan(lse[0, 1, H - 1])
+    out[0, 1, H - 1], lse[0, 1, H - 1] = good[0][0, 1, H - 1], good[1][0, 1, H - 1]
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("H", [4, 40])
+def test_views_and_an_empty_cache(cuda, H):
+    # tensors that start inside their storage, one that wants a gradient, and a cache of no rows
+    dims = kp.make_dims(H)
+    c = case(np.random.default_rng(9), "fp8", 2, 3, H, 100, [100, 50], [3, 2], n_rows=300)
+    d = device_args(c, cuda, dims)
+    inside = {k: torch.cat([v[:1], v])[1:] if isinstance(v, torch.Tensor) and k != "workspace" else v for k, v in d.items()}
+    assert inside["q"].storage_offset() > 0 and inside["q"].is_contiguous()
+    inside["q"].requires_grad_()
+    CALL["fp8"](dims, **inside)
+    torch.cuda.synchronize()
+    check(c, inside["out"], inside["lse"])
+    none = dict(c, rows=np.full((2, 100), -1, np.int32))
+    d["rows"].fill_(-1)
+    d["cache"] = d["cache"][:0]
+    CALL["fp8"](dims, **d)
+    torch.cuda.synchronize()
+    check(none, d["out"], d["lse"])
+
+
+def test_output_over_the_query_is_refused(cuda):
+    dims = kp.make_dims(4)
+    c = case(np.random.default_rng(10), "int8", 1, 2, 4, 70, [70], [2])
+    d = device_args(c, cuda, dims)
+    with pytest.raises(kp.GlmError):
+        CALL["int8"](dims, **dict(d, out=d["q"]))
+
+
+def test_the_widest_list(cuda):
+    # 1,024 rows 1,024 times over: their softmax is that of the rows once, lse by log 1024 more
+    rng = np.random.default_rng(11)
+    n = 1 << 20
+    c = case(rng, "int8", 1, 1, 2, 1024, [1024], [1], n_rows=1024)
+    wide = dict(c, rows=np.tile(c["rows"], (1, 1024)), row_len=np.array([n], np.int32), masks=[[0]])
+    out, lse = launch(wide, cuda)
+    c["masks"] = [[0]]
+    q = synth.bf16_bits_to_f32(c["q"]).astype(np.float64)
+    (_, _, want, wl, tol, ltol), = R.tree(q, c["cache"], c["rows"], c["row_len"], c["draft"], c["masks"], c["n_tree"], SM, "int8")
+    more = n / 8 * R.U32                                  # the sums of tests/tree_reference.py, over n rows
+    v = R.values(c["cache"], c["rows"][0], "int8")
+    s = (q[0, 0] @ v.T) * SM
+    p = np.exp(s - wl[:, None])
+    o, l = out[0, 0].float().cpu().numpy(), lse[0, 0].cpu().numpy()
+    assert (np.abs(o - want) <= tol + more * (p @ np.abs(v))).all()
+    assert (np.abs(l - (wl + np.log(1024))) <= ltol + more).all()
+
+
+@pytest.mark.parametrize("B,T,H,width", [(20000, 1, 1, 3), (1, 64, 128, 90), (2, 64, 128, 700)])
+def test_the_largest_batch_and_trees(cuda, B, T, H, width):
+    rng = np.random.default_rng(12)
+    c = case(rng, "fp4", B, T, H, width, [int(v) for v in rng.integers(0, width + 1, B)], [int(v) for v in rng.integers(0, T + 1, B)],
+             n_rows=300)
+    check(c, *launch(c, cuda))
