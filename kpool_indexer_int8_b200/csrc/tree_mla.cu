@@ -120,12 +120,13 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     const int H = a.n_heads;
     const int n_rows_q = a.n_nodes * H;                       // query rows of the sequence; this CTA's: r0 .. r0 + NQ - 1
     const bool direct = parts == 1;
+    const Lengths own = load_lengths(a, b, true), mine = load_lengths(a, lane, !direct && lane < a.batch);
     for (int i = tid; i < min(NQ, n_rows_q - r0) * 8; i += kThreads)   // (read when the lengths are there)
         prefetch_line(a.q + (static_cast<int64_t>(b) * n_rows_q + r0) * kLatent + i * 64);
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
-    const int plen = list_len(a, b), tree_n = tree_len(a, b);
+    const int plen = list_len(a, own), tree_n = tree_len(a, own);
     const int prefix = (plen + kTrKeys - 1) / kTrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
-    const int run = direct ? tiles : run_tiles(a, plan, kTrKeys, tiles);
+    const int run = direct ? tiles : run_tiles(a, plan, kTrKeys, mine);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
     const int live = tree_n * H - r0;                         // of this CTA's query rows, those of the tree

@@ -14,31 +14,34 @@ constexpr float kGrow = 12.0f;                 // a score passes its reference b
 constexpr float kSpread = 2.0f;                // a row scale is at most 2 sigma
 constexpr float kBoost = 4.0f;                 // P' <= 2^12 * 2 * 4 = 2^15 < 65504
 
-// The keys of a sequence in tiles: the index list's, then one tile of drafted rows.
-__device__ __forceinline__ int list_len(const TreeArgs &a, int b) {
-    return a.row_len ? min(max(a.row_len[b], 0), a.width) : a.width;
+// The keys of a sequence in tiles: the index list's, then one tile of drafted rows. The lengths as they are
+// in memory are asked for first of all in a kernel and used as late as can be.
+struct Lengths {
+    int list, tree;
+};
+__device__ __forceinline__ Lengths load_lengths(const TreeArgs &a, int b, bool there) {
+    return {there && a.row_len ? a.row_len[b] : a.width, there && a.n_tree ? a.n_tree[b] : a.n_nodes};
 }
-__device__ __forceinline__ int tree_len(const TreeArgs &a, int b) {
-    return a.n_tree ? min(max(a.n_tree[b], 0), a.n_nodes) : a.n_nodes;
-}
-__device__ __forceinline__ int tile_count(const TreeArgs &a, int b, int keys) {
-    return (list_len(a, b) + keys - 1) / keys + (tree_len(a, b) > 0 ? 1 : 0);
+__device__ __forceinline__ int list_len(const TreeArgs &a, Lengths n) { return min(max(n.list, 0), a.width); }
+__device__ __forceinline__ int tree_len(const TreeArgs &a, Lengths n) { return min(max(n.tree, 0), a.n_nodes); }
+__device__ __forceinline__ int tile_count(const TreeArgs &a, Lengths n, int keys) {
+    return (list_len(a, n) + keys - 1) / keys + (tree_len(a, n) > 0 ? 1 : 0);
 }
 // The tiles of a part: every sequence is cut into runs of as many, the length for which the busiest
 // of `units` SMs (or pairs) is done first, a run costing about six tiles more than its own (set-up,
 // output): up to `levels` waves of runs are tried, one when there is nothing to balance. Computed
-// by every warp for itself from the device's list lengths (own: the tiles of this CTA's sequence).
-__device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, int keys, int own) {
+// by every warp for itself from the device's list lengths (mine: those of sequence `lane`).
+__device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, int keys, Lengths mine) {
     const int lane = threadIdx.x & 31;
     auto reduce = [](int v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
-    const int first = a.batch == 1 ? (lane == 0 ? own : 0) : (lane < a.batch ? tile_count(a, lane, keys) : 0);
+    const int first = lane < a.batch ? tile_count(a, mine, keys) : 0;
     int sum = 0, most = 0;
     for (int s = lane; s < a.batch; s += 32) {
-        const int n = s < 32 ? first : tile_count(a, s, keys);
+        const int n = s < 32 ? first : tile_count(a, load_lengths(a, s, true), keys);
         sum += n;
         most = max(most, n);
     }
@@ -52,7 +55,7 @@ __device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, i
         int run = max(low, (sum + target - 1) / target), n = 0;
         for (int it = 0; it < 8; it++) {
             n = 0;
-            for (int s = lane; s < a.batch; s += 32) n += ((s < 32 ? first : tile_count(a, s, keys)) + run - 1) / run;
+            for (int s = lane; s < a.batch; s += 32) n += ((s < 32 ? first : tile_count(a, load_lengths(a, s, true), keys)) + run - 1) / run;
             n = reduce(n);
             if (n <= target || run >= most) break;
             run = max(run + 1, static_cast<int>(static_cast<int64_t>(run) * n / target));

@@ -67,6 +67,7 @@ struct PrLayout {
     static constexpr int kTmem = kBar + kPbCount * 8;
     static constexpr int kBytes = kTmem + 8;
     static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
+    static_assert(kPrRows == 16 * kPrSoft, "query rows of a softmax warp");
     static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 8 == 0 && kFull % 16 == 0 && kMax % 16 == 0 && kK % 1024 == 0 &&
                       kV % 1024 == 0 && kKBlock % 1024 == 0 && kVBlock % 1024 == 0 && kRawK % 128 == 0 && kRawV % 128 == 0, "alignment");
     static_assert(kAlloc <= 232448 && kPrRows * kPartRow <= kP, "shared memory of one CTA");
@@ -126,16 +127,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     const int parts = plan.parts;
     const bool direct = parts == 1;
 
-    // the query rows as they are, where K and V will be (rows 16 bytes apart in the banks)
+    const Lengths own = load_lengths(a, b, true), mine = load_lengths(a, lane, !direct && lane < a.batch);
+    if (warp < kPrSoft) {
+        // The softmax warps: the query rows as fp16, each scaled by the power of two that puts its largest
+        // magnitude in [2^14, 2^15), by way of shared memory where K and V will be (rows 16 bytes apart in the
+        // banks), a warp two groups of 8 rows and four lanes a row. Rolled loops, and before the lengths are
+        // there: held in registers, unrolled and after them, it took 12,000 cycles of a first call's 48,000.
+        // (Rows that no node of the tree has are converted like the others; they are put out as empty.)
 #pragma unroll 1
-    for (int i = tid; i < kPrRows * 64; i += kPrThreads)
-        copy16(smem + L::kK + (i >> 6) * L::kOutRow + (i & 63) * 16,
-               a.q + (static_cast<int64_t>(b) * n_rows_q + min(r0 + (i >> 6), n_rows_q - 1)) * kLatent + (i & 63) * 8, true);
-    copy_commit();
+        for (int i = 0; i < 16 * 32; i += 32) {
+            const int row = warp * 16 + i / 32;
+            const uint16_t *from = a.q + (static_cast<int64_t>(b) * n_rows_q + min(r0 + row, n_rows_q - 1)) * kLatent;
+            copy16(smem + L::kK + row * L::kOutRow + lane * 16, from + lane * 8, true);
+            copy16(smem + L::kK + row * L::kOutRow + (lane + 32) * 16, from + (lane + 32) * 8, true);
+        }
+        copy_commit();
+        copy_wait<0>();
+#pragma unroll 1
+        for (int g = 2 * warp; g < 2 * warp + 2; g++) {
+            const int qr = g * 8 + (lane & 7);
+            const unsigned char *from = smem + L::kK + qr * L::kOutRow + (lane >> 3) * 16;
+            unsigned mx = 0u;
+#pragma unroll 8
+            for (int i = 0; i < 16; i++) mx = max(mx, bf16_absmax(*reinterpret_cast<const uint4 *>(from + 64 * i)));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const int e = query_exponent(mx);
+            const float f = pow2f_exact(e);
+            if (lane < 8) rowk[qr] = a.sm_scale * 1.4426950408889634f * pow2f_exact(-e);
+            unsigned char *to = smem + L::kQ + g * 8192 + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll 1
+            for (int i = 0; i < 16; i += 4) {
+                uint4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) v[k] = *reinterpret_cast<const uint4 *>(from + 64 * (i + k));
+#pragma unroll
+                for (int k = 0; k < 4; k++) *reinterpret_cast<uint4 *>(to + 4 * (i + k) * 128) = bf16_to_f16x8(v[k], f);
+            }
+        }
+        tc::fence_proxy_async();
+    }
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
-    const int plen = list_len(a, b), tree_n = tree_len(a, b);
+    const int plen = list_len(a, own), tree_n = tree_len(a, own);
     const int prefix = (plen + kPrKeys - 1) / kPrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
-    const int run = direct ? tiles : run_tiles(a, plan, kPrKeys, tiles);
+    const int run = direct ? tiles : run_tiles(a, plan, kPrKeys, mine);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
     const int live = tree_n * H;                             // query rows of the tree
@@ -147,7 +182,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         return ((static_cast<int64_t>(b) * a.n_nodes + node) * parts + part) * H + (r - node * H);
     };
     if (n_tiles == 0) {   // no key for the pair, or no node of the tree
-        copy_wait<0>();
         if (direct)
             for (int i = tid; i < kPrRows * 64; i += kPrThreads) {
                 const int r = r0 + (i >> 6);
@@ -184,34 +218,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             tc::mbar_fence_init();
         }
     }
-    // Every warp calls it once, with its first cache rows requested: the query rows as fp16, each scaled by
-    // the power of two that puts its largest magnitude in [2^14, 2^15), by the first warps a group of 8
-    // each, a row by four lanes; then the barriers and tensor memory of both CTAs are there. (Rolled loops,
-    // from shared memory: held in registers and unrolled, it took 12,000 cycles of a first call's 48,000,
-    // for its instructions.)
+    // Every warp calls it once, with its first cache rows requested: the query, the barriers and tensor
+    // memory of both CTAs are there behind it.
     uint32_t tmem;
     auto start = [&]() {
-        named_sync(0, kPrThreads);
-        if (warp < kPrRows / 8) {
-            const int qr = warp * 8 + (lane & 7);
-            const bool real = r0 + qr < live;
-            const unsigned char *from = smem + L::kK + qr * L::kOutRow + (lane >> 3) * 16;
-            unsigned mx = 0u;
-#pragma unroll 4
-            for (int i = 0; i < 16; i++) mx = max(mx, bf16_absmax(*reinterpret_cast<const uint4 *>(from + 64 * i)));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const int e = query_exponent(mx);
-            const float f = pow2f_exact(e);
-            if (lane < 8) rowk[qr] = a.sm_scale * 1.4426950408889634f * pow2f_exact(-e);
-            unsigned char *to = smem + L::kQ + warp * 8192 + (lane >> 3) * 128 + (lane & 7) * 16;
-#pragma unroll 2
-            for (int i = 0; i < 16; i++) {
-                const uint4 v = bf16_to_f16x8(*reinterpret_cast<const uint4 *>(from + 64 * i), f);
-                *reinterpret_cast<uint4 *>(to + 4 * i * 128) = real ? v : make_uint4(0u, 0u, 0u, 0u);
-            }
-            tc::fence_proxy_async();
-        }
         named_sync(0, kPrThreads);
         cluster_sync();
         tc::fence_after_sync();
@@ -256,7 +266,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
         copy_commit();
         float sc = other_scale(t0, rows);
-        copy_wait<1>();                                        // (the query rows)
         start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
@@ -326,7 +335,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         int e1 = entry(t0 + 1);
         R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
         copy_commit();
-        copy_wait<1>();                                        // (the query rows)
         start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i;
@@ -353,7 +361,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else if (warp == kPrWarpMma) {
         // ---------------- tensor cores (the first CTA's, for both) ----------------
-        copy_wait<0>();
         start();
         if (cta == 0) {
             constexpr uint32_t id_s = tc::idesc_f16(128, kPrKeys, false, false);
@@ -398,7 +405,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         }
     } else {
         // ---------------- softmax ----------------
-        copy_wait<0>();
         start();
 
         // tensor-memory lane 32 warp + lane: row, and the lower or upper 48 keys of a tile

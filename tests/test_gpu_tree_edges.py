@@ -356,3 +356,20 @@ def test_the_largest_batch_and_trees(cuda, B, T, H, width):
     c = case(rng, "fp4", B, T, H, width, [int(v) for v in rng.integers(0, width + 1, B)], [int(v) for v in rng.integers(0, T + 1, B)],
              n_rows=300)
     check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("H,width", [(4, 300), (20, 3000), (64, 300), (64, 3000)])
+def test_what_unused_nodes_hold_means_nothing(cuda, H, width):
+    # queries, masks and drafted rows past a tree's nodes: NaN, infinities, bits everywhere
+    rng = np.random.default_rng(13)
+    c = case(rng, "fp8", 3, 5, H, width, [width, 10, 0], [3, 0, 1], n_rows=400)
+    q = bf16(c["q"]).clone()
+    for b, t in enumerate(c["n_tree"]):
+        q[b, t:, ::2], q[b, t:, 1::2] = float("nan"), float("inf")
+        c["masks"][b][t:] = [-1] * (5 - t)
+        c["draft"][b * 5 + t:b * 5 + 5] = 0xFF
+    c["q"] = q.view(torch.int16).numpy().view(np.uint16)
+    out, lse = launch(c, cuda)
+    plain = q.clone()
+    plain[~torch.isfinite(plain)] = 0.0
+    check(dict(c, q=plain.view(torch.int16).numpy().view(np.uint16)), out, lse)
