@@ -218,11 +218,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             tc::mbar_fence_init();
         }
     }
-    // Every warp calls it once, with its first cache rows requested: the query, the barriers and tensor
-    // memory of both CTAs are there behind it.
-    uint32_t tmem;
+    // Every warp calls it once, before it first needs the query, the barriers or tensor memory of both CTAs
+    // (it joins all threads of both).
+    uint32_t tmem = 0;
     auto start = [&]() {
-        named_sync(0, kPrThreads);
+        __syncwarp();
         cluster_sync();
         tc::fence_after_sync();
         tmem = *tmem_slot;
@@ -266,7 +266,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
         copy_commit();
         float sc = other_scale(t0, rows);
-        start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
             const bool drafts = t >= prefix;
@@ -299,6 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             copy_commit();
             const float sc_next = other_scale(t + 1, nxt);
             if (i > 0) wait(kPbS + ((i - 1) & 1), (i - 1) >> 1);   // S(t - 1) is done: K is free
+            else start();
             if (holds) {
                 scl[m * kPrKeys + my_key] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
                 val[m * kPrKeys + my_key] = rows >= 0 ? 1 : 0;
@@ -335,7 +335,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         int e1 = entry(t0 + 1);
         R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
         copy_commit();
-        start();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i;
             const bool drafts = t >= prefix;
@@ -350,6 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             if (i + 1 < n_tiles) R::template fetch_half<kN>(codes, tails, base_of(t + 1), nxt, cta);
             copy_commit();
             if (i > 0) wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);   // O of t - 1 is done: V is free
+            else start();
             unsigned char *to = smem + L::kV + (lane >> 3) * L::kVBlock;
 #pragma unroll
             for (int r = 0; r < kN; r++)
