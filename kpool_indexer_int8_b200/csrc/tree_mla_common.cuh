@@ -29,8 +29,10 @@ __device__ __forceinline__ int tile_count(const TreeArgs &a, Lengths n, int keys
 }
 // The tiles of a part: every sequence is cut into runs of as many, the length for which the busiest
 // of `units` SMs (or pairs) is done first, a run costing about six tiles more than its own (set-up,
-// output): up to `levels` waves of runs are tried, one when there is nothing to balance. Computed
-// by every warp for itself from the device's list lengths (mine: those of sequence `lane`).
+// output): up to `levels` waves of runs are tried, one when there is nothing to balance. A run counts once
+// for each tile of query rows that the sequence's tree fills (4 trees of 8 to 13 nodes: 53.6 us a call, 54.3
+// with all counted as full). Computed by every warp for itself from the device's lengths (mine: those
+// of sequence `lane`).
 __device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, int keys, Lengths mine) {
     const int lane = threadIdx.x & 31;
     auto reduce = [](int v) {
@@ -38,29 +40,37 @@ __device__ __forceinline__ int run_tiles(const TreeArgs &a, const TreePlan &p, i
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     };
-    const int first = lane < a.batch ? tile_count(a, mine, keys) : 0;
+    auto weight = [&](Lengths n) { return (tree_len(a, n) * a.n_heads + p.nq - 1) / p.nq; };
+    const int first = lane < a.batch ? tile_count(a, mine, keys) : 0, first_w = lane < a.batch ? weight(mine) : 0;
+    // f(tiles, weight) over all sequences, this lane's share
+    auto each = [&](auto f) {
+        if (lane < a.batch) f(first, first_w);
+        for (int s = lane + 32; s < a.batch; s += 32) {
+            const Lengths n = load_lengths(a, s, true);
+            f(tile_count(a, n, keys), weight(n));
+        }
+    };
     int sum = 0, most = 0;
-    for (int s = lane; s < a.batch; s += 32) {
-        const int n = s < 32 ? first : tile_count(a, load_lengths(a, s, true), keys);
-        sum += n;
-        most = max(most, n);
-    }
+    each([&](int tiles, int w) {
+        sum += tiles * w;
+        most = max(most, tiles);
+    });
     sum = reduce(sum);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     const int low = max(1, (most + p.parts - 1) / p.parts);
-    int best = max(low, 1), best_cost = 0x7fffffff;
+    int best = low, best_cost = 0x7fffffff;
     for (int k = 1; k <= p.levels; k++) {
-        const int target = max(1, k * p.units / p.q_tiles);   // runs of one query tile over all sequences
+        const int target = k * p.units;
         int run = max(low, (sum + target - 1) / target), n = 0;
         for (int it = 0; it < 8; it++) {
             n = 0;
-            for (int s = lane; s < a.batch; s += 32) n += ((s < 32 ? first : tile_count(a, load_lengths(a, s, true), keys)) + run - 1) / run;
+            each([&](int tiles, int w) { n += (tiles + run - 1) / run * w; });
             n = reduce(n);
             if (n <= target || run >= most) break;
             run = max(run + 1, static_cast<int>(static_cast<int64_t>(run) * n / target));
         }
-        const int cost = (n * p.q_tiles + p.units - 1) / p.units * (run + 6);
+        const int cost = (n + p.units - 1) / p.units * (run + 6);
         if (cost < best_cost) {
             best_cost = cost;
             best = run;
