@@ -31,7 +31,7 @@
 // two are in flight: a 64-key tile takes 3,300 cycles, where shared memory (C written once and read twice)
 // would allow 2,000. 262,144 4-bit rows, 16 query rows: 73 us a call with the merge, 1.1 TB/s; the rows at
 // the copy rate would take 12. A small call is bound by its start and end and, cold, by its
-// instructions: 67 int8 keys and 64 query rows take 11.4 us of the GPU, merge
+// instructions: 67 int8 keys and 64 query rows take 11.1 us of the GPU, merge
 // included.
 #include "tree_mla_common.cuh"
 

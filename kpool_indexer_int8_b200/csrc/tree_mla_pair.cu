@@ -20,7 +20,7 @@
 // shared-memory wavefronts of the warps (counted; rows copied in and read, 49 KB each way, K and V 48 KB each
 // and P 12 KB written, scales, barriers) and 184 KB of operands read by the tensor cores (Q 64, K 48, V
 // 48, P twice 12), 1,470 cycles: 3,700. Tensor pipe 42 % active, issue 46 %. 8 nodes of 64 heads over
-// 262,144 int8 rows: 380 us a call, 720 TFLOP/s (350 us and 780 alone on a cool chip), 0.44 of the
+// 262,144 int8 rows: 372 us a call, 740 TFLOP/s (350 us and 785 alone on a cool chip), 0.45 of the
 // measured bf16 rate. What was tried on top of it and did not pay: two teams of softmax warps on alternate
 // tiles (410 us), eight softmax warps on one tile (386), rows read in rolled loops right before they are
 // widened (390-404), one set of warps for K and V (391).
