@@ -580,11 +580,12 @@ def _bad(t, dtype, shape, name, device):
     return ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _take(device, *named):
-    """Addresses of the tensors of a call, checked: (tensor or None, dtype, shape or None, name) each, all
+def _take(device, tensors, dtypes, shapes, names):
+    """Addresses of the tensors (or None) of a call, checked against their types and shapes (None: any), all
     contiguous on one device. The checks of a decode step's calls are on its critical path, so they are
     native; a tensor that fails them (or that the native code cannot see) is looked at again here."""
-    return _args.take(device, *named) or [_address(device, *n) for n in named]
+    return _args.take(device, tensors, dtypes, shapes) or \
+        [_address(device, *n) for n in zip(tensors, dtypes, shapes, names)]
 
 
 def _address(device, t, dtype, shape, name):
@@ -619,6 +620,10 @@ def _need(t, name, ndim):
 _I8, _U8, _T32, _T64, _BF = torch.int8, torch.uint8, torch.int32, torch.int64, torch.bfloat16
 
 
+_TREE_NAMES = ("q", "cache", "rows", "row_len", "draft", "mask", "n_tree", "out", "lse", "workspace")
+_TREE_TYPES = {kind: (_BF, kind, _T32, _T32, kind, _T64, _T32, _BF, torch.float32, _U8) for kind in (_I8, _U8)}
+
+
 def _tree_mla(fn, name, dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse, row_len, n_tree, stream, kind,
               row_bytes):
     shape, dev = _need(q, "q", 4)
@@ -626,10 +631,9 @@ def _tree_mla(fn, name, dims, q, cache, rows, draft, mask, sm_scale, out, worksp
     if rows.dim() != 2:
         raise ValueError(f"rows must have 2 dims, got {rows.dim()}")
     width, ws_bytes, per_seq = rows.shape[1], workspace.numel(), (B,)
-    p = _take(dev, (q, _BF, (B, T, dims.n_heads, 512), "q"), (cache, kind, None, "cache"), (rows, _T32, (B, width), "rows"),
-              (row_len, _T32, per_seq, "row_len"), (draft, kind, None, "draft"), (mask, _T64, (B, T), "mask"),
-              (n_tree, _T32, per_seq, "n_tree"), (out, _BF, shape, "out"), (lse, torch.float32, (B, T, H), "lse"),
-              (workspace, _U8, None, "workspace"))
+    p = _take(dev, (q, cache, rows, row_len, draft, mask, n_tree, out, lse, workspace), _TREE_TYPES[kind],
+              ((B, T, dims.n_heads, 512), None, (B, width), per_seq, None, (B, T), per_seq, shape, (B, T, dims.n_heads), None),
+              _TREE_NAMES)
     if draft.numel() != B * T * row_bytes:
         raise ValueError(f"draft must hold {B * T} rows of {row_bytes} bytes, got {draft.numel()} bytes")
     _call(fn, name, dev, stream, C.byref(dims), p[0], p[1], cache.numel() // row_bytes, p[2], p[3], width, p[4], p[5], p[6], B,
@@ -660,6 +664,11 @@ def glm_tree_mla_decode_fp4(dims, q, cache, rows, draft, mask, sm_scale, out, wo
               workspace, lse, row_len, n_tree, stream, _U8, GLM_FP4_ROW_BYTES)
 
 
+_TABLES_NAMES = ("length", "n_new", "n_blocks", "pad", "block_table", "free", "n_free", "slots", "q_seq", "q_pos", "slot_map",
+                 "len_out", "n_blocks_out", "cu_new", "free_out", "n_free_out")
+_TABLES_TYPES = tuple(_T64 if name in ("slots", "slot_map") else _T32 for name in _TABLES_NAMES)
+
+
 def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_size, pool_blocks, slots, q_seq, q_pos,
                      len_out, n_blocks_out, cu_new, free_out, n_free_out, pad=None, slot_map=None, stream=None) -> None:
     """Block tables, slots and slot maps from request lengths: length, n_new, n_blocks (pad) int32 [B];
@@ -671,18 +680,20 @@ def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_s
     B, ld_blocks = block_table.shape
     ld_slot = 0 if slot_map is None else slot_map.shape[-1]
     packed, pool, one = slots.shape, free.shape, (1,)
-    p = _take(dev, (length, _T32, None, "length"), (n_new, _T32, per_seq, "n_new"), (n_blocks, _T32, per_seq, "n_blocks"),
-              (pad, _T32, per_seq, "pad"), (block_table, _T32, (per_seq[0], ld_blocks), "block_table"),
-              (free, _T32, None, "free"), (n_free, _T32, one, "n_free"), (slots, _T64, None, "slots"),
-              (q_seq, _T32, packed, "q_seq"), (q_pos, _T32, packed, "q_pos"), (slot_map, _T64, (B, ld_slot), "slot_map"),
-              (len_out, _T32, per_seq, "len_out"), (n_blocks_out, _T32, per_seq, "n_blocks_out"),
-              (cu_new, _T32, (B + 1,), "cu_new"), (free_out, _T32, pool, "free_out"), (n_free_out, _T32, one, "n_free_out"))
+    p = _take(dev, (length, n_new, n_blocks, pad, block_table, free, n_free, slots, q_seq, q_pos, slot_map, len_out, n_blocks_out,
+                    cu_new, free_out, n_free_out), _TABLES_TYPES,
+              (None, per_seq, per_seq, per_seq, (B, ld_blocks), None, one, None, packed, packed, (B, ld_slot), per_seq, per_seq,
+               (B + 1,), pool, one), _TABLES_NAMES)
     _call(lib.glm_block_tables, "glm_block_tables", dev, stream, p[0], p[1], p[2], p[3], B, block_size, p[4], ld_blocks, p[5],
           p[6], free.numel(), pool_blocks, p[7], p[8], p[9], slots.numel(), p[10], ld_slot, p[11], p[12], p[13], p[14], p[15])
 
 
 _COMMIT_FORMAT = {(torch.int8, GLM_ROW_BYTES): GLM_CACHE_INT8, (torch.uint8, GLM_ROW_BYTES): GLM_CACHE_FP8,
                   (torch.uint8, GLM_FP4_ROW_BYTES): GLM_CACHE_FP4}
+
+
+_COMMIT_NAMES = ("draft", "path", "slots", "q_seq", "q_pos", "cu_new", "cache", "draft_k", "draft_gate", "k", "gate")
+_COMMIT_TYPES = {kind: (kind, _T32, _T64, _T32, _T32, _T32, kind, _BF, _BF, _BF, _BF) for kind in (_I8, _U8)}
 
 
 def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cache, draft_k=None, draft_gate=None,
@@ -698,9 +709,7 @@ def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cac
         raise ValueError(f"draft and cache must be rows of one format, got {kind} rows of {row} and {cache.shape[-1]}")
     ld_tokens = 0 if k is None else k.shape[1]
     drafts, state = (B, n_nodes, 128), (B, ld_tokens, 128)
-    p = _take(dev, (draft, kind, (B * n_nodes, row), "draft"), (path, _T32, None, "path"), (slots, _T64, None, "slots"),
-              (q_seq, _T32, packed, "q_seq"), (q_pos, _T32, packed, "q_pos"), (cu_new, _T32, (B + 1,), "cu_new"),
-              (cache, kind, None, "cache"), (draft_k, _BF, drafts, "draft_k"), (draft_gate, _BF, drafts, "draft_gate"),
-              (k, _BF, state, "k"), (gate, _BF, state, "gate"))
+    p = _take(dev, (draft, path, slots, q_seq, q_pos, cu_new, cache, draft_k, draft_gate, k, gate), _COMMIT_TYPES[kind],
+              ((B * n_nodes, row), None, None, packed, packed, (B + 1,), None, drafts, drafts, state, state), _COMMIT_NAMES)
     _call(lib.glm_tree_commit, "glm_tree_commit", dev, stream, C.byref(dims), p[0], fmt, p[1], B, n_nodes, ld_path, p[2], p[3],
           p[4], p[5], slots.numel(), p[6], cache.numel() // row, p[7], p[8], p[9], p[10], ld_tokens)

@@ -47,8 +47,7 @@ static PyObject *setup(PyObject *self, PyObject *args) {
     Py_RETURN_NONE;
 }
 
-static int fits(PyObject *spec, long device, DLTensor *d) {
-    PyObject *t = PyTuple_GET_ITEM(spec, 0), *dtype = PyTuple_GET_ITEM(spec, 1), *shape = PyTuple_GET_ITEM(spec, 2);
+static int fits(PyObject *t, PyObject *dtype, PyObject *shape, long device, DLTensor *d) {
     if (!PyObject_TypeCheck(t, tensor_type)) return 0;
     if (api->dltensor_from_py_object_no_sync(t, d) != 0) {
         PyErr_Clear();
@@ -75,25 +74,24 @@ static int fits(PyObject *spec, long device, DLTensor *d) {
     return 1;
 }
 
-/* take(device, (tensor or None, dtype, shape or None, name), ...): a list of addresses (None for None), or
- * None when a tensor is not as it should be. */
-static PyObject *take(PyObject *self, PyObject *const *args, Py_ssize_t n) {
-    if (n < 1 || !api) return PyErr_Format(PyExc_TypeError, "take(device, ...) after setup()");
+/* take(device, tensors, dtypes, shapes): tuples of one length, of tensors or None, of their types and of their
+ * shapes or None. A list of addresses (None for None), or None when a tensor is not as it should be. */
+static PyObject *take(PyObject *self, PyObject *const *args, Py_ssize_t n_args) {
+    if (n_args != 4 || !api || !PyTuple_Check(args[1]) || !PyTuple_Check(args[2]) || !PyTuple_Check(args[3]))
+        return PyErr_Format(PyExc_TypeError, "take(device, tensors, dtypes, shapes) after setup()");
+    const Py_ssize_t n = PyTuple_GET_SIZE(args[1]);
+    if (PyTuple_GET_SIZE(args[2]) != n || PyTuple_GET_SIZE(args[3]) != n)
+        return PyErr_Format(PyExc_TypeError, "tuples of one length are expected");
     const long device = PyLong_AsLong(args[0]);
     if (device == -1 && PyErr_Occurred()) return NULL;
-    PyObject *out = PyList_New(n - 1);
+    PyObject *out = PyList_New(n);
     if (!out) return NULL;
-    for (Py_ssize_t i = 1; i < n; i++) {
-        PyObject *spec = args[i], *p = NULL;
+    for (Py_ssize_t i = 0; i < n; i++) {
+        PyObject *t = PyTuple_GET_ITEM(args[1], i), *p = Py_None;
         DLTensor d;
-        if (!PyTuple_Check(spec) || PyTuple_GET_SIZE(spec) != 4) {
-            Py_DECREF(out);
-            return PyErr_Format(PyExc_TypeError, "(tensor, dtype, shape, name) is expected");
-        }
-        if (PyTuple_GET_ITEM(spec, 0) == Py_None) {
-            p = Py_None;
+        if (t == Py_None) {
             Py_INCREF(p);
-        } else if (fits(spec, device, &d)) {
+        } else if (fits(t, PyTuple_GET_ITEM(args[2], i), PyTuple_GET_ITEM(args[3], i), device, &d)) {
             p = PyLong_FromVoidPtr(d.data ? (char *)d.data + d.byte_offset : NULL);
             if (!p) {
                 Py_DECREF(out);
@@ -103,7 +101,7 @@ static PyObject *take(PyObject *self, PyObject *const *args, Py_ssize_t n) {
             Py_DECREF(out);
             Py_RETURN_NONE;
         }
-        PyList_SET_ITEM(out, i - 1, p);
+        PyList_SET_ITEM(out, i, p);
     }
     return out;
 }
