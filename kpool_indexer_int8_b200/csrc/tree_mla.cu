@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         prefetch_line(a.q + (static_cast<int64_t>(b) * n_rows_q + r0) * kLatent + i * 64);
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
     const int plen = list_len(a, own), tree_n = tree_len(a, own);
-    const int prefix = (plen + kTrKeys - 1) / kTrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
+    const int n_keys = plen + tree_n, tiles = (n_keys + kTrKeys - 1) / kTrKeys;
     const int run = direct ? tiles : run_tiles(a, plan, kTrKeys, mine);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
@@ -171,17 +171,17 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     const int k = w * kN + lane;
     auto entry_of = [&](int t) -> int {
         if (t >= t1 || lane >= kN) return -1;
-        if (t >= prefix) return k < tree_n ? b * a.n_nodes + k : -1;
         const int j = t * kTrKeys + k;
-        return j < plen ? __ldg(list + j) : -1;
+        if (j < plen) return __ldg(list + j);
+        return j < n_keys ? draft_row(b * a.n_nodes + j - plen) : -1;
     };
-    auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
+    auto row_of = [&](int t, int entry) { return t * kTrKeys + k >= plen || (entry >= 0 && entry < a.n_rows) ? entry : -1; };
     // starts copying group g (of four rows; kGt groups a tile, counted from the run's first); `rows`:
     // what the lanes hold of its tile
     auto request = [&](int g, int rows) {
         if (g < kGt * n_tiles)
-            R::template fetch<4>(codes + g % kG * 4 * R::kCodes, tails + g % kG * 4 * R::kTail,
-                                 t0 + g / kGt < prefix ? a.cache : a.draft, rows, g % kGt * 4);
+            R::template fetch<4>(codes + g % kG * 4 * R::kCodes, tails + g % kG * 4 * R::kTail, a, rows, g % kGt * 4,
+                                 (t0 + g / kGt + 1) * kTrKeys > plen);
         copy_commit();
     };
     // rows of tiles i .. i + 2, entries of the one after; the first copies go out before the barriers are there
@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         // ---------------- widening: keys kN w .. kN w + kN - 1 of each tile ----------------
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, buf = i & 1;
-            const bool drafts = t >= prefix;
-            const bool valid = rows[0] >= 0;
+            const bool drafts = (t + 1) * kTrKeys > plen;     // some of its keys are
+            const bool valid = rows[0] != -1;
             float sc = 0.0f;
 #pragma unroll
             for (int h = 0; h < kGt; h++) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 copy_wait<kG - 1>();                          // the group is there
                 unsigned char *first = codes + g % kG * 4 * R::kCodes, *tail = tails + g % kG * 4 * R::kTail;
                 if (valid && lane / 4 == h) sc = R::scale(tail + (lane & 3) * R::kTail);
-                if (kFmt != kFmtInt8 && drafts) {   // a drafted row with NaN codes: its scale makes every score with it NaN
+                if (kFmt != kFmtInt8 && drafts) {   // a row with NaN codes: its scale makes every score with it NaN
                     for (int r = 0; r < 4; r++)
                         if (R::has_nan(first + r * R::kCodes, tail + r * R::kTail) && lane == h * 4 + r && valid) sc = __int_as_float(0x7fc00000);
                     R::clean(R::kFp4 ? tail : first, 4 * (R::kFp4 ? R::kTail : R::kCodes));
@@ -393,10 +393,12 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                     x[e + 1] = fmaf(__uint_as_float(r[e + 1]) * f.z, sc, f.w == kTrNone ? 0.0f : -f.w);
                 }
             }
-            if (!key || t >= prefix) {
+            const int draft = t * kTrKeys + j - plen;             // which of the drafts the key is, if any
+            const bool drafts = (t + 1) * kTrKeys > plen;
+            if (!key || drafts) {
 #pragma unroll
-                for (int e = 0; e < V; e++)
-                    if (!key || !((mask[c0 + e] >> j) & 1ull)) x[e] = -INFINITY;   // what each node sees of the drafts
+                for (int e = 0; e < V; e++)   // what each node sees of the drafts
+                    if (!key || (draft >= 0 && !((mask[c0 + e] >> (draft & 63)) & 1ull))) x[e] = -INFINITY;
             }
             float top = -INFINITY;
 #pragma unroll
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                     l[8 * g + e] += p0;
                     l[8 * g + e + 1] += p1;
                     p4[e >> 1] = f16x2_rn(p0 * ratio, p1 * ratio);
-                    if (t >= prefix) {   // a draft that the node does not see may have any scale
+                    if (drafts) {   // a draft that the node does not see may have any scale
                         if (x[8 * g + e] == -INFINITY) p4[e >> 1] &= 0xffff0000u;
                         if (x[8 * g + e + 1] == -INFINITY) p4[e >> 1] &= 0x0000ffffu;
                     }
@@ -585,6 +587,7 @@ TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms) 
     if (batch > 1 && parts > 1) parts *= 2;    // a list twice as long as the mean
     if (parts > tiles) parts = tiles;
     if (parts > kTrMaxParts) parts = kTrMaxParts;
+    if (small && tiles <= 3) parts = 1;
     p.parts = static_cast<int>(parts < 1 ? 1 : parts);
     return p;
 }

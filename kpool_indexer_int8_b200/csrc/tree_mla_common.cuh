@@ -14,7 +14,7 @@ constexpr float kGrow = 12.0f;                 // a score passes its reference b
 constexpr float kSpread = 2.0f;                // a row scale is at most 2 sigma
 constexpr float kBoost = 4.0f;                 // P' <= 2^12 * 2 * 4 = 2^15 < 65504
 
-// The keys of a sequence in tiles: the index list's, then one tile of drafted rows. The lengths as they are
+// The keys of a sequence: those of the index list, then the drafted rows, in tiles. The lengths as they are
 // in memory are asked for first of all in a kernel and used as late as can be.
 struct Lengths {
     int list, tree;
@@ -25,8 +25,10 @@ __device__ __forceinline__ Lengths load_lengths(const TreeArgs &a, int b, bool t
 __device__ __forceinline__ int list_len(const TreeArgs &a, Lengths n) { return min(max(n.list, 0), a.width); }
 __device__ __forceinline__ int tree_len(const TreeArgs &a, Lengths n) { return min(max(n.tree, 0), a.n_nodes); }
 __device__ __forceinline__ int tile_count(const TreeArgs &a, Lengths n, int keys) {
-    return (list_len(a, n) + keys - 1) / keys + (tree_len(a, n) > 0 ? 1 : 0);
+    return (list_len(a, n) + tree_len(a, n) + keys - 1) / keys;
 }
+// A key's row: a cache row, or one of `draft` as -2 - its index there; -1: none.
+__device__ __forceinline__ int draft_row(int index) { return -2 - index; }
 // The tiles of a part: every sequence is cut into runs of as many, the length for which the busiest
 // of `units` SMs (or pairs) is done first, a run costing about six tiles more than its own (set-up,
 // output): up to `levels` waves of runs are tried, one when there is nothing to balance. A run counts once
@@ -118,47 +120,71 @@ struct Row {
     static constexpr int kTail = kBytes - kCodes;
     static constexpr int kSclAt = (kFp4 ? kFp4RowScaleAt : kLatent) - kCodes;   // the row scale in the tail
 
+    __device__ __forceinline__ static const uint8_t *at(const TreeArgs &a, int row) {
+        return (row >= 0 ? a.cache : a.draft) + static_cast<int64_t>(row >= 0 ? row : max(-2 - row, 0)) * kBytes;
+    }
     // One warp starts copying the NR rows that lanes lane0 .. lane0 + NR - 1 hold (-1: zeros) to codes
-    // [NR][kCodes] and tails [NR][kTail] in shared memory. No branch, so that the copies go out back to back.
+    // [NR][kCodes] and tails [NR][kTail] in shared memory; mixed: some may be drafts (a tile in a list, and a
+    // rolled loop: looking for them in every tile cost 3 % of a long call). No branch on a row, so that the
+    // copies go out back to back.
     template <int NR>
-    __device__ __forceinline__ static void fetch(unsigned char *codes, unsigned char *tails, const uint8_t *base, int rows,
-                                                 int lane0) {
+    __device__ __forceinline__ static void fetch(unsigned char *codes, unsigned char *tails, const TreeArgs &a, int rows,
+                                                 int lane0, bool mixed) {
         constexpr int kPer = 512 / kCodes, kTp = kTail / 16;      // rows of a copy, pieces of a tail
         static_assert(NR % kPer == 0 && NR <= 32, "rows of a group");
-        const int lane = threadIdx.x & 31, at = (lane * 16) % kCodes;
-        int r[NR / kPer];
+        const int lane = threadIdx.x & 31, piece = (lane * 16) % kCodes;
+        auto code = [&](int i, auto from) {
+            const int r = __shfl_sync(0xffffffffu, rows, lane0 + i * kPer + lane * 16 / kCodes);
+            copy16(codes + i * 512 + lane * 16, from(r) + piece, r != -1);
+        };
+        auto tail = [&](int i, auto from) {
+            const int p = i + lane, r = __shfl_sync(0xffffffffu, rows, lane0 + min(p / kTp, NR - 1));
+            if (p < NR * kTp) copy16(tails + p * 16, from(r) + kCodes + p % kTp * 16, r != -1);
+        };
+        if (mixed) {
+            auto from = [&](int r) { return at(a, r); };
+#pragma unroll 1
+            for (int i = 0; i < NR / kPer; i++) code(i, from);
+#pragma unroll 1
+            for (int i = 0; i < NR * kTp; i += 32) tail(i, from);
+        } else {
+            auto from = [&](int r) { return a.cache + static_cast<int64_t>(max(r, 0)) * kBytes; };
 #pragma unroll
-        for (int i = 0; i < NR / kPer; i++) r[i] = __shfl_sync(0xffffffffu, rows, lane0 + i * kPer + lane * 16 / kCodes);
+            for (int i = 0; i < NR / kPer; i++) code(i, from);
 #pragma unroll
-        for (int i = 0; i < NR / kPer; i++)
-            copy16(codes + i * 512 + lane * 16, base + static_cast<int64_t>(max(r[i], 0)) * kBytes + at, r[i] >= 0);
-#pragma unroll
-        for (int i = 0; i < NR * kTp; i += 32) {
-            const int p = i + lane, rt = __shfl_sync(0xffffffffu, rows, lane0 + min(p / kTp, NR - 1));
-            if (p < NR * kTp) copy16(tails + p * 16, base + static_cast<int64_t>(max(rt, 0)) * kBytes + kCodes + p % kTp * 16, rt >= 0);
+            for (int i = 0; i < NR * kTp; i += 32) tail(i, from);
         }
     }
     // The same for the codes of dims 128 part + [0, 128) of each 256 (half a row: 256 or 128 bytes of
     // codes, both parts of a row behind each other), and the whole tails of 4-bit rows.
     template <int NR>
-    __device__ __forceinline__ static void fetch_half(unsigned char *codes, unsigned char *tails, const uint8_t *base, int rows,
-                                                      int part) {
+    __device__ __forceinline__ static void fetch_half(unsigned char *codes, unsigned char *tails, const TreeArgs &a, int rows,
+                                                      int part, bool mixed) {
         constexpr int kHalf = kCodes / 2, kPer = 512 / kHalf, kSeg = kHalf / 2;
         static_assert(NR % kPer == 0 && NR <= 32, "rows of a group");
         const int lane = threadIdx.x & 31, in = (lane * 16) % kHalf;
-        const int at = (in / kSeg) * kHalf + part * kSeg + in % kSeg;
-        int r[NR / kPer];
+        const int piece = (in / kSeg) * kHalf + part * kSeg + in % kSeg;
+        auto code = [&](int i, auto from) {
+            const int r = __shfl_sync(0xffffffffu, rows, i * kPer + lane * 16 / kHalf);
+            copy16(codes + i * 512 + lane * 16, from(r) + piece, r != -1);
+        };
+        auto tail = [&](int i, auto from) {
+            const int p = i + lane, r = __shfl_sync(0xffffffffu, rows, min(p / 3, NR - 1));
+            if (p < NR * 3) copy16(tails + p * 16, from(r) + kCodes + p % 3 * 16, r != -1);
+        };
+        constexpr int kTails = kFp4 ? NR * 3 : 0;
+        if (mixed) {
+            auto from = [&](int r) { return at(a, r); };
+#pragma unroll 1
+            for (int i = 0; i < NR / kPer; i++) code(i, from);
+#pragma unroll 1
+            for (int i = 0; i < kTails; i += 32) tail(i, from);
+        } else {
+            auto from = [&](int r) { return a.cache + static_cast<int64_t>(max(r, 0)) * kBytes; };
 #pragma unroll
-        for (int i = 0; i < NR / kPer; i++) r[i] = __shfl_sync(0xffffffffu, rows, i * kPer + lane * 16 / kHalf);
+            for (int i = 0; i < NR / kPer; i++) code(i, from);
 #pragma unroll
-        for (int i = 0; i < NR / kPer; i++)
-            copy16(codes + i * 512 + lane * 16, base + static_cast<int64_t>(max(r[i], 0)) * kBytes + at, r[i] >= 0);
-        if constexpr (kFp4) {
-#pragma unroll
-            for (int i = 0; i < NR * 3; i += 32) {
-                const int p = i + lane, rt = __shfl_sync(0xffffffffu, rows, min(p / 3, NR - 1));
-                if (p < NR * 3) copy16(tails + p * 16, base + static_cast<int64_t>(max(rt, 0)) * kBytes + kCodes + p % 3 * 16, rt >= 0);
-            }
+            for (int i = 0; i < kTails; i += 32) tail(i, from);
         }
     }
     __device__ __forceinline__ static float scale(const unsigned char *tail) { return *reinterpret_cast<const float *>(tail + kSclAt); }

@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     }
     // the sequence's tiles [0, tiles), those of the list first, and this part's [t0, t1)
     const int plen = list_len(a, own), tree_n = tree_len(a, own);
-    const int prefix = (plen + kPrKeys - 1) / kPrKeys, tiles = prefix + (tree_n > 0 ? 1 : 0);
+    const int n_keys = plen + tree_n, tiles = (n_keys + kPrKeys - 1) / kPrKeys;
     const int run = direct ? tiles : run_tiles(a, plan, kPrKeys, mine);
     const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(part) * run));
     const int t1 = min(tiles, t0 + run);
@@ -236,13 +236,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     // the list's entry (or drafted row) of key `key` of tile t, and the row it means, -1: none. (An entry
     // is looked at only when its row is needed: a test right behind the load would hold the warp.)
     auto entry_of = [&](int t, int key) -> int {
-        if (t >= t1) return -1;
-        if (t >= prefix) return key < tree_n ? b * a.n_nodes + key : -1;
         const int j = t * kPrKeys + key;
-        return j < plen ? __ldg(list + j) : -1;
+        if (t >= t1) return -1;
+        if (j < plen) return __ldg(list + j);
+        return j < n_keys ? draft_row(b * a.n_nodes + j - plen) : -1;
     };
-    auto row_of = [&](int t, int entry) { return entry >= 0 && (t >= prefix || entry < a.n_rows) ? entry : -1; };
-    auto base_of = [&](int t) { return t < prefix ? a.cache : a.draft; };
+    auto row_of = [&](int t, int key, int entry) {
+        return t * kPrKeys + key >= plen || (entry >= 0 && entry < a.n_rows) ? entry : -1;
+    };
+    auto has_drafts = [&](int t) { return (t + 1) * kPrKeys > plen; };
 
     if (warp >= kPrSoft && warp < kPrWarpV) {
         // ---------------- K: keys 8 w .. 8 w + 7 of this CTA's half of each tile, whole rows ----------------
@@ -256,29 +258,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         unsigned char *tails = smem + L::kRawK + kPrHalf * R::kCodes + w * kN * R::kTail;
         auto entry = [&](int t) { return holds ? entry_of(t, my_key) : -1; };
         // the scale of a row of the other half (its own rows' scales come with them)
-        auto other_scale = [&](int t, int row) {
-            return which && row >= 0 ? __ldg(reinterpret_cast<const float *>(base_of(t) + static_cast<int64_t>(row) * R::kBytes +
-                                                                            R::kCodes + R::kSclAt))
-                                     : 0.0f;
+        auto other_scale = [&](int row) {
+            return which && row != -1 ? __ldg(reinterpret_cast<const float *>(R::at(a, row) + R::kCodes + R::kSclAt)) : 0.0f;
         };
         int e1 = entry(t0 + 1);
-        int rows = row_of(t0, entry(t0));
-        R::template fetch<kN>(codes, tails, base_of(t0), rows, 0);
+        int rows = row_of(t0, my_key, entry(t0));
+        R::template fetch<kN>(codes, tails, a, rows, 0, has_drafts(t0));
         copy_commit();
-        float sc = other_scale(t0, rows);
+        float sc = other_scale(rows);
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
-            const bool drafts = t >= prefix;
+            const bool drafts = has_drafts(t);
             const int e2 = entry(t + 2);
             copy_wait<0>();
             if (lane < kN) sc = R::scale(tails + lane * R::kTail);
-            if (kFmt != kFmtInt8 && drafts) {   // a drafted row with NaN codes: its scale makes every score with it NaN
+            if (kFmt != kFmtInt8 && drafts) {   // a row with NaN codes: its scale makes every score with it NaN
                 unsigned bad = 0u;
 #pragma unroll 8
                 for (int r = 0; r < 32; r++) {
                     const int row = __shfl_sync(0xffffffffu, rows, r);
-                    const uint8_t *p = a.draft + static_cast<int64_t>(max(row, 0)) * R::kBytes;
-                    if (row >= 0 && R::nan_share(p, p + R::kCodes)) bad |= 1u << r;
+                    const uint8_t *p = R::at(a, row);
+                    if (row != -1 && R::nan_share(p, p + R::kCodes)) bad |= 1u << r;
                 }
                 if (__reduce_or_sync(0xffffffffu, bad) >> lane & 1u) sc = __int_as_float(0x7fc00000);
             }
@@ -290,18 +290,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; h++)
                     v[r][h] = R::line(codes + r * R::kCodes, tails + r * R::kTail, lane + 32 * h, lane / 2 + 16 * h);
-            const unsigned bits = __ballot_sync(0xffffffffu, rows >= 0);
+            const unsigned bits = __ballot_sync(0xffffffffu, rows != -1);
             const float mx = finite_max(holds ? sc : 0.0f);
             // the next rows, into the slots just read
-            const int nxt = row_of(t + 1, e1);
-            if (i + 1 < n_tiles) R::template fetch<kN>(codes, tails, base_of(t + 1), nxt, 0);
+            const int nxt = row_of(t + 1, my_key, e1);
+            if (i + 1 < n_tiles) R::template fetch<kN>(codes, tails, a, nxt, 0, has_drafts(t + 1));
             copy_commit();
-            const float sc_next = other_scale(t + 1, nxt);
+            const float sc_next = other_scale(nxt);
             if (i > 0) wait(kPbS + ((i - 1) & 1), (i - 1) >> 1);   // S(t - 1) is done: K is free
             else start();
             if (holds) {
                 scl[m * kPrKeys + my_key] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
-                val[m * kPrKeys + my_key] = rows >= 0 ? 1 : 0;
+                val[m * kPrKeys + my_key] = rows != -1 ? 1 : 0;
             }
             if (lane == 0) {
                 smx[m * 8 + w] = mx;
@@ -330,23 +330,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         const int w = warp - kPrWarpV;
         unsigned char *codes = smem + L::kRawV + w * kN * (R::kCodes / 2);
         unsigned char *tails = smem + L::kRawV + kPrKeys * (R::kCodes / 2) + w * kN * R::kTail;   // (4-bit rows)
-        auto entry = [&](int t) { return lane < kN ? entry_of(t, w * kN + lane) : -1; };
+        const int my_key = w * kN + lane;
+        auto entry = [&](int t) { return lane < kN ? entry_of(t, my_key) : -1; };
         const int block = (lane >> 4) * 16 + cta * 8 + (lane & 15) / 2;
         int e1 = entry(t0 + 1);
-        R::template fetch_half<kN>(codes, tails, base_of(t0), row_of(t0, entry(t0)), cta);
+        R::template fetch_half<kN>(codes, tails, a, row_of(t0, my_key, entry(t0)), cta, has_drafts(t0));
         copy_commit();
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i;
-            const bool drafts = t >= prefix;
+            const bool drafts = has_drafts(t);
             const int e2 = entry(t + 2);
             copy_wait<0>();
             if (kFmt != kFmtInt8 && drafts) R::clean(R::kFp4 ? tails : codes, kN * (R::kFp4 ? R::kTail : R::kCodes / 2));
             typename R::Line v[kN];
 #pragma unroll
             for (int r = 0; r < kN; r++) v[r] = R::line(codes + r * (R::kCodes / 2), tails + r * R::kTail, lane, block);
-            const int nxt = row_of(t + 1, e1);
+            const int nxt = row_of(t + 1, my_key, e1);
             __syncwarp();
-            if (i + 1 < n_tiles) R::template fetch_half<kN>(codes, tails, base_of(t + 1), nxt, cta);
+            if (i + 1 < n_tiles) R::template fetch_half<kN>(codes, tails, a, nxt, cta, has_drafts(t + 1));
             copy_commit();
             if (i > 0) wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);   // O of t - 1 is done: V is free
             else start();
@@ -443,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 }
             }
             const uint2 fw = *reinterpret_cast<const uint2 *>(full + m * 16 + half * 8);
-            const bool partial = (fw.x & fw.y) != 0x01010101u || t >= prefix;
+            const bool partial = (fw.x & fw.y) != 0x01010101u || has_drafts(t);
             uint64_t keys = (1ull << kPrHalf) - 1;                      // this thread's keys
             if (partial) {
                 const uint2 *vb = reinterpret_cast<const uint2 *>(val + m * kPrKeys + key0);
@@ -454,7 +455,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                     const uint2 v = vb[g];
                     keys |= static_cast<uint64_t>(((v.x * 0x10204080u) >> 28) | (((v.y * 0x10204080u) >> 28) << 4)) << (8 * g);
                 }
-                if (t >= prefix) keys &= seen >> key0;                  // what the node sees of the drafts
+                if (has_drafts(t)) {                                    // what the node sees of the drafts
+                    const int n = plen - t * kPrKeys - key0;            // this thread's first draft
+                    keys &= n >= kPrHalf ? ~0ull : (n > 0 ? ((1ull << n) - 1) | seen << n : (n > -64 ? seen >> -n : 0ull));
+                }
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e++)
                     if (!((keys >> e) & 1ull)) x[e] = -INFINITY;
