@@ -1,10 +1,10 @@
 // block_tables.cu -- block tables, slots and slot maps from request lengths, and the copy of
 // accepted drafts into the slots so made. Both are bound by latency at decode sizes, so each is one
 // launch: every CTA of the tables kernel scans the requests for itself (a few microseconds' worth
-// of loads that all CTAs do at once) instead of waiting for a scan kernel. On the GPU a call takes 4.5 us
-// for 8 requests with a token each, 5.2 for 200 with up to 8, 7.7 for 16 prompts of up to 32,768 tokens
+// of loads that all CTAs do at once) instead of waiting for a scan kernel. On the GPU a call takes 4.7 us
+// for 8 requests with a token each, 5.4 for 200 with up to 8, 7.9 for 16 prompts of up to 32,768 tokens
 // (6.8 MB of slots, positions and maps: 1.0 at the copy rate); the commit 1.9 for 4 tokens or 380. From
-// Python the host's call is longer than either: 9.6 and 8.5 us.
+// Python the host's call is longer than either: 9.1 and 8.1 us.
 #include <algorithm>
 
 #include "block_tables.cuh"
