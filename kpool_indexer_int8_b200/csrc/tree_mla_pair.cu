@@ -16,14 +16,14 @@
 //   * warp 14 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs.
 // K, V and P have one buffer each: shared memory holds no more beside Q.
 //
-// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,680 cycles of a CTA: 2,230 cycles of
+// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,645 cycles of a CTA: 2,150 cycles of
 // shared-memory wavefronts of the warps (counted; rows copied in and read, 49 KB each way, K and V 48 KB each
-// and P 12 KB written, scales, barriers) and 184 KB of operands read by the tensor cores (Q 64, K 48, V
-// 48, P twice 12), 1,470 cycles: 3,700. Tensor pipe 42 % active, issue 46 %. 8 nodes of 64 heads over
-// 262,144 int8 rows: 372 us a call, 740 TFLOP/s (350 us and 785 alone on a cool chip), 0.45 of the
-// measured bf16 rate. What was tried on top of it and did not pay: two teams of softmax warps on alternate
-// tiles (410 us), eight softmax warps on one tile (386), rows read in rolled loops right before they are
-// widened (390-404), one set of warps for K and V (391).
+// and P 12 KB written, scales, barriers) and 172 KB of operands read by the tensor cores (Q 64, K 48, V
+// 48, P 12), 1,380 cycles: 97 %. Tensor pipe 42 % active, issue 46 %. 8 nodes of 64 heads over 262,144
+// int8 rows: 369 us a call, 745 TFLOP/s (350 us and 785 alone on a cool chip), 0.45 of the measured
+// bf16 rate; 372 with P read for each of its two products. What was tried on top of it and did not pay:
+// two teams of softmax warps on alternate tiles (410 us), eight softmax warps on one tile (386), rows read
+// in rolled loops right before they are widened (390-404), one set of warps for K and V (391).
 #include "tree_mla_common.cuh"
 
 namespace glm {
@@ -93,6 +93,16 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// The two products of one A: the first keeps it beside the tensor core, the second takes it from there.
+__device__ __forceinline__ void mma_pair_twice(uint32_t d0, uint32_t d1, uint64_t a, uint64_t b0, uint64_t b1, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], %2, %3, %5, p;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%1], %2, %4, %5, p;\n\t}\n" ::"r"(d0),
+        "r"(d1), "l"(a), "l"(b0), "l"(b1), "r"(idesc), "r"(accumulate));
 }
 // Arrive on the barrier of this offset in both CTAs when the products issued so far are done.
 __device__ __forceinline__ void commit_pair(uint32_t mbar) {
@@ -378,10 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 if (tc::elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kPrKeys / 16; ks++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++)
-                            mma_pair(tmem + j * 128, dp + ((ks * 256) >> 4), dv + ((ks * 2048 + j * 2 * L::kVBlock) >> 4), id_o,
-                                     (i > 0 || ks > 0) ? 1u : 0u);
+                        mma_pair_twice(tmem, tmem + 128, dp + ((ks * 256) >> 4), dv + ((ks * 2048) >> 4),
+                                       dv + ((ks * 2048 + 2 * L::kVBlock) >> 4), id_o, (i > 0 || ks > 0) ? 1u : 0u);
                     commit_pair(bar(kPbDone + (i & 1)));
                 }
                 __syncwarp();
