@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     const uint32_t bar0 = tc::smem_addr(smem + L::kBar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
 
-    const int b = blockIdx.x / plan.q_tiles, r0 = (blockIdx.x - b * plan.q_tiles) * NQ, part = blockIdx.y, parts = plan.parts;
+    const int r0 = blockIdx.x * NQ, part = blockIdx.y, b = blockIdx.z, parts = plan.parts;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int H = a.n_heads;
@@ -557,7 +557,7 @@ cudaError_t launch_tree_t(const TreePlan &p, const TreeArgs &a, float *part_acc,
     const int smem = TrLayout<NQ>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, dim3(a.batch * p.q_tiles, p.parts), dim3(TrLayout<NQ>::kThreads), smem, stream, a, p, part_acc, part_ml);
+    e = launch_pdl(kernel, dim3(p.q_tiles, p.parts, a.batch), dim3(TrLayout<NQ>::kThreads), smem, stream, a, p, part_acc, part_ml);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
