@@ -1,8 +1,8 @@
 // tree_combine.cu -- the merge of the tree attention's partial softmax states.
 //
 // A query row's partials hold, over the keys of their run, acc = sum 2^(..) v, the sum l of the weights and
-// their reference m (natural units); with M = max m over the partials with l > 0 the row is
-//     out = sum e^(m - M) acc / sum e^(m - M) l,    lse = M + log(sum e^(m - M) l),
+// their reference m (log2 units, a whole number); with M = max m over the partials with l > 0 the row is
+//     out = sum 2^(m - M) acc / sum 2^(m - M) l,    lse = M log 2 + log(sum 2^(m - M) l),
 // all of it in fp32, in the same order every time. It is bound by the partials' 2 KB each, which the
 // attention has just written and L2 holds, and for few rows by the number of loads in flight. With as many
 // rows as SMs, a row is one CTA of 128 threads, a thread four dims, eight partials in flight (3,328 rows
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kFew ? 32 * kTcWarps : 128) tree_combine_kerne
         const bool real = j0 + lane < mine;
         const float2 s = real ? ml[first + static_cast<int64_t>(off + (j0 + lane) * step) * n_heads] : make_float2(-INFINITY, 0.0f);
         const bool there = s.x > -INFINITY;
-        const float w = there ? expf(s.x - top) : 0.0f;
+        const float w = there ? exp2f(s.x - top) : 0.0f;
         l += there ? w * s.y : 0.0f;
         const unsigned live = __ballot_sync(0xffffffffu, there);
         const int n = min(32, mine - j0);
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kFew ? 32 * kTcWarps : 128) tree_combine_kerne
     const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), hi = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
     *reinterpret_cast<uint2 *>(out + row * kLatent + dim) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    if (lse && dim == 0) lse[row] = none ? -INFINITY : top + logf(l);
+    if (lse && dim == 0) lse[row] = none ? -INFINITY : top * 0.6931471805599453f + logf(l);
 }
 
 }  // namespace

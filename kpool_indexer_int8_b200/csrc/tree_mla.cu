@@ -15,13 +15,12 @@
 //     128 bytes in the 128-byte swizzle, which the tensor cores read both as keys and, transposed, as values;
 //   * warp 16 (tensor cores): S^T(t) = C(t) . Q^T into one of two accumulators, O^T += C(t)^T P(t)^T,
 //     whichever is ready first;
-//   * warps 0-7 (softmax): x = S scale_row qk - ref in log2 units, P' = 2^x scale_row 4 / sigma as fp16.
-//     The reference of a query row moves only when a score passes it by 2^12 (a vote of the eight
-//     warps per tile), and sigma, a power of two, only when a row scale passes 2 sigma: then the
-//     accumulator in tensor memory is rescaled, otherwise no maximum is taken. Sums stay in
-//     registers, one per thread and query row, until the end.
-// P' <= 2^15 is one fp16 term: a weight is off by at most 2^-11 of itself (an eighth of the bf16
-// output's 2^-8), or by 2^-25 sigma / 4 once P' is below 2^-14.
+//   * warps 0-7 (softmax): x = S scale_row qk - ref in log2 units, P' = 2^x scale_row / sigma as fp16, with a
+//     reference and a sigma for each query row. They move only when a weight of the row would pass 2^15 (a
+//     vote of the eight warps per tile): then the accumulator in tensor memory is rescaled, otherwise no
+//     maximum is taken. Sums stay in registers, one per thread and query row, until the end.
+// P' is one fp16 term: a weight is off by at most 2^-11 of itself (an eighth of the bf16 output's 2^-8), or,
+// once P' is below 2^-14, by 2^-24 - kHead of the row's largest weight times scale.
 //
 // A sequence's keys are cut into runs so that the CTAs fill the SMs; tree_combine.cu merges the
 // partials. Every wait is bounded; one that gives up sets the status word and the CTA writes NaN.
@@ -42,7 +41,6 @@ using namespace tree;
 
 constexpr int kTrSoft = 8;                     // warps 0-7 softmax, then the widening warps and one for the tensor cores
 constexpr int kTrKeys = 64;                    // keys of a tile
-constexpr float kTrNone = -1e30f;              // reference of a query row that has seen no key
 
 enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbCount = 10 };
 
@@ -61,18 +59,18 @@ struct TrLayout {
     static constexpr int kFac = kRaw + kWiden * kGroups * 4 * kRowBytes;                // [NQ] (score factor, reference) pairs
     static constexpr int kMask = kFac + NQ * 8;                  // [NQ] visibility words
     static constexpr int kOut = kMask + NQ * 8;                  // [NQ] row of the output or partial, -1: none
-    static constexpr int kRed = kOut + NQ * 8;                   // [4 quadrants][NQ]
-    static constexpr int kAlpha = kRed + 4 * NQ * 4;             // [NQ] factors of a rescale, at the end of the output
-    static constexpr int kScl = kAlpha + NQ * 4;                 // [2][64] row scales
-    static constexpr int kMax = kScl + 2 * kTrKeys * 4;          // [2][16] largest finite scale of a warp's rows
-    static constexpr int kValid = kMax + 2 * 16 * 4;              // [2][64] bytes: 1 where there is a key
+    static constexpr int kRed = kOut + NQ * 8;                   // [2][4 quadrants][NQ]
+    static constexpr int kAlpha = kRed + 2 * 4 * NQ * 4;         // [NQ] factors of a rescale, at the end of the output
+    static constexpr int kSigma = kAlpha + NQ * 4;               // [NQ] 1 / sigma
+    static constexpr int kLog = kSigma + NQ * 4;                 // [NQ] log2 sigma, -infinity: no reference yet
+    static constexpr int kScl = kLog + NQ * 4;                   // [2][64] row scales
+    static constexpr int kValid = kScl + 2 * kTrKeys * 4;        // [2][64] bytes: 1 where there is a key
     static constexpr int kQmax = kValid + 2 * kTrKeys;                    // [NQ] |q| maxima (bf16 bits)
-    static constexpr int kNone = kQmax + NQ * 4;                 // query rows without a reference
-    static constexpr int kBar = kNone + 8;
+    static constexpr int kBar = kQmax + NQ * 4;
     static constexpr int kTmem = kBar + kTbCount * 8;
     static constexpr int kBytes = kTmem + 8;
     static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
-    static_assert(kQ % 128 == 0 && kP % 128 == 0 && kFac % 16 == 0 && kBar % 8 == 0 && kMask % 8 == 0 && kMax % 16 == 0,
+    static_assert(kQ % 128 == 0 && kP % 128 == 0 && kFac % 16 == 0 && kBar % 8 == 0 && kMask % 8 == 0 && kSigma % 16 == 0 && kLog % 16 == 0,
                   "alignment");
     static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
@@ -105,10 +103,10 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     float *red = reinterpret_cast<float *>(smem + L::kRed);
     float *alpha = reinterpret_cast<float *>(smem + L::kAlpha);
     float *scl = reinterpret_cast<float *>(smem + L::kScl);
-    float *smx = reinterpret_cast<float *>(smem + L::kMax);
+    float *inv = reinterpret_cast<float *>(smem + L::kSigma);
+    float *log_sigma = reinterpret_cast<float *>(smem + L::kLog);
     uint8_t *val = reinterpret_cast<uint8_t *>(smem + L::kValid);
     unsigned *qmax = reinterpret_cast<unsigned *>(smem + L::kQmax);
-    int *n_none = reinterpret_cast<int *>(smem + L::kNone);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmem);
     const uint32_t bar0 = tc::smem_addr(smem + L::kBar);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -217,8 +215,11 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         if (lane < 8) atomicMax(&qmax[qr], mx);
         named_sync(1, 256);
         const float f = pow2f_exact(query_exponent(qmax[qr]));
-        if (tid < NQ)
-            fac[tid] = make_float2(a.sm_scale * 1.4426950408889634f * pow2f_exact(-query_exponent(qmax[tid])), kTrNone);
+        if (tid < NQ) {
+            fac[tid] = make_float2(a.sm_scale * 1.4426950408889634f * pow2f_exact(-query_exponent(qmax[tid])), 0.0f);
+            inv[tid] = 1.0f;
+            log_sigma[tid] = -INFINITY;
+        }
 #pragma unroll
         for (int i = 0; i < kN; i++)
             *reinterpret_cast<uint4 *>(smem + L::kQ + (qr >> 3) * 8192 + (p0 + i * kStride) * 128 + (qr & 7) * 16) =
@@ -238,7 +239,6 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tc::mbar_init(bar(kTbP + i), 8);
             }
             tc::mbar_fence_init();
-            *n_none = NQ;
         }
     }
     __syncthreads();
@@ -286,12 +286,10 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                     for (int u = 0; u < 2; u++) *reinterpret_cast<uint4 *>(to + u * 4 * 8192) = R::widen(v[r][u]);
                 }
             }
-            const float m = finite_max(sc);
             if (lane < kN) {
                 scl[buf * kTrKeys + k] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
                 val[buf * kTrKeys + k] = valid ? 1 : 0;
             }
-            if (lane == 0) smx[buf * 16 + w] = m;
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(kTbFull + buf));
@@ -359,24 +357,48 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         float l[V];
 #pragma unroll
         for (int e = 0; e < V; e++) l[e] = 0.0f;
-        float sigma = 0.0f;
-        bool pending = true;                                      // some query row has no reference yet
-        const float4 *f4 = reinterpret_cast<const float4 *>(fac + c0);
+        const float4 *f4 = reinterpret_cast<const float4 *>(fac + c0), *log4 = reinterpret_cast<const float4 *>(log_sigma + c0);
+        const float4 *inv4 = reinterpret_cast<const float4 *>(inv + c0);
         for (int i = 0; i < n_tiles; i++) {
             const int buf = i & 1, t = t0 + i;
             wait(kTbFull + buf, i >> 1);                          // (the tile's scales and valid rows)
             const bool key = lane < 16 && val[buf * kTrKeys + j] != 0;
             const float sc = key ? scl[buf * kTrKeys + j] : 0.0f;
-            float smax = 0.0f;
+            // What a row's score may be beyond kTop: its p, and p scale / sigma, at most 2^kTop (a row without a reference:
+            // none). And scale / sigma: a scale far above sigma, or a NaN, has a weight of 0, or the score is NaN; the product
+            // of the weight with it must be 0 too. Up to 32 query rows: while S is being made.
+            float most[V], over[V];
+            const float lg = sc > 0.0f ? __log2f(sc) : -150.0f;
+            auto load_most = [&]() {
 #pragma unroll
-            for (int e = 0; e < L::kWiden / 4; e++) {
-                const float4 v = reinterpret_cast<const float4 *>(smx + buf * 16)[e];
-                smax = max3(smax, fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                for (int e = 0; e < V; e += 4) {
+                    const float4 f = log4[e >> 2];
+                    most[e] = fminf(0.0f, f.x - lg);
+                    most[e + 1] = fminf(0.0f, f.y - lg);
+                    most[e + 2] = fminf(0.0f, f.z - lg);
+                    most[e + 3] = fminf(0.0f, f.w - lg);
+                }
+            };
+            auto load_over = [&](int e0, int n) {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    if (e < e0 || e >= e0 + n) continue;
+                    const float4 f = inv4[e >> 2];
+                    over[e] = fminf(sc * f.x, kFltMax);
+                    over[e + 1] = fminf(sc * f.y, kFltMax);
+                    over[e + 2] = fminf(sc * f.z, kFltMax);
+                    over[e + 3] = fminf(sc * f.w, kFltMax);
+                }
+            };
+            constexpr bool kEarly = V <= 16;
+            if constexpr (kEarly) {
+                load_most();
+                load_over(0, V);
             }
             wait(kTbS + buf, i >> 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
-            // the scores of this thread's key less the references (0 for a row that has none)
+            // the scores of this thread's key less the references
             float x[V];
             {
                 uint32_t r[V];
@@ -388,8 +410,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
                     const float4 f = f4[e >> 1];
-                    x[e] = fmaf(__uint_as_float(r[e]) * f.x, sc, f.y == kTrNone ? 0.0f : -f.y);
-                    x[e + 1] = fmaf(__uint_as_float(r[e + 1]) * f.z, sc, f.w == kTrNone ? 0.0f : -f.w);
+                    x[e] = fmaf(__uint_as_float(r[e]) * f.x, sc, -f.y);
+                    x[e + 1] = fmaf(__uint_as_float(r[e + 1]) * f.z, sc, -f.w);
                 }
             }
             const int draft = t * kTrKeys + j - plen;             // which of the drafts the key is, if any
@@ -399,40 +421,49 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 for (int e = 0; e < V; e++)   // what each node sees of the drafts
                     if (!key || (draft >= 0 && !((mask[c0 + e] >> (draft & 63)) & 1ull))) x[e] = -INFINITY;
             }
-            float top = -INFINITY;
+            if constexpr (!kEarly) load_most();
+            float past = -INFINITY;                               // (the maximum passes over what is NaN)
 #pragma unroll
-            for (int e = 0; e < V; e++) top = fmaxf(top, x[e]);
-            const bool grow = smax > kSpread * sigma;               // (sigma 0: no scale yet)
-            if (named_or(1, 256, top > kGrow) || grow || pending) {
-                // move the references and sigma, and rescale what they scale
+            for (int e = 0; e < V; e += 2) past = max3(past, x[e] - most[e], x[e + 1] - most[e + 1]);
+            if (named_or(1, 256, past > kTop)) {
+                // move the references and sigmas that have to, and rescale what they scale
+                const int at = quad * NQ + c0 + ((lane >> kShift) & (V - 1));
                 float m[V];
 #pragma unroll
                 for (int e = 0; e < V; e++) m[e] = x[e];
-                const float bm = butterfly<V, true>(m);
-                if ((lane & kLow) == 0) red[quad * NQ + c0 + ((lane >> kShift) & (V - 1))] = bm;
-                const float sig_new = grow ? sigma_of(smax) : sigma;
-                const float beta = sigma == 0.0f ? 1.0f : sigma / sig_new;   // powers of two: exact
-                sigma = sig_new;
-                if (tid == 0) *n_none = 0;
-                named_sync(1, 256);
-                float delta = 0.0f;
-                if (tid < NQ) {
-                    const float mc = fmaxf(fmaxf(red[tid], red[NQ + tid]), fmaxf(red[2 * NQ + tid], red[3 * NQ + tid]));
-                    const bool none = fac[tid].y == kTrNone;
-                    if (mc > (none ? -INFINITY : kGrow)) delta = mc;
-                    if (mc > -INFINITY || !none) fac[tid].y = (none ? 0.0f : fac[tid].y) + delta;
-                    else atomicAdd(n_none, 1);
-                    alpha[tid] = none ? 0.0f : exp2f(-delta);
-                    red[tid] = delta;
+                const float bx = butterfly<V, true>(m), ls = sc > 0.0f ? lg : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < V; e++) m[e] = x[e] + ls;
+                const float by = butterfly<V, true>(m);
+                if ((lane & kLow) == 0) {
+                    red[at] = bx;
+                    red[4 * NQ + at] = by;
                 }
                 named_sync(1, 256);
-                pending = *n_none > 0;
+                float fo = 1.0f;
+                if (tid < NQ) {
+                    const float *rx = red + tid, *ry = red + 4 * NQ + tid;
+                    const float mx = fmaxf(fmaxf(rx[0], rx[NQ]), fmaxf(rx[2 * NQ], rx[3 * NQ]));
+                    const float my = fmaxf(fmaxf(ry[0], ry[NQ]), fmaxf(ry[2 * NQ], ry[3 * NQ]));
+                    const float old = fac[tid].y;
+                    Scaling s{old, log_sigma[tid], log_sigma[tid] == -INFINITY};
+                    float fl;
+                    move_scaling(s, mx, my, fl, fo);
+                    fac[tid].y = s.ref;
+                    log_sigma[tid] = s.log_sigma;
+                    if (!s.none) inv[tid] = pow2f_exact(-static_cast<int>(s.log_sigma));
+                    alpha[tid] = fo;
+                    red[tid] = s.ref == old ? 0.0f : s.ref - old;
+                    red[4 * NQ + tid] = fl;
+                }
+                const bool rescale = named_or(1, 256, fo != 1.0f);
 #pragma unroll
                 for (int e = 0; e < V; e++) {
-                    l[e] *= alpha[c0 + e];
+                    l[e] *= red[4 * NQ + c0 + e];
                     x[e] -= red[c0 + e];
                 }
-                if (i > 0) {
+                if constexpr (kEarly) load_over(0, V);
+                if (rescale && i > 0) {
                     wait(kTbDone + ((i - 1) & 1), (i - 1) >> 1);
                     ok = __all_sync(0xffffffffu, ok);
                     tc::fence_after_sync();
@@ -445,33 +476,27 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                             tr_tmem_ld<CH>(tmem + lanes + mt * NQ + cb, o);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < CH; e++)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[cb + e] * beta));
+                            for (int e = 0; e < CH; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[cb + e]);
                             tc::tmem_st16(tmem + lanes + mt * NQ + cb, o);
                         }
                     }
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                 }
-                named_sync(1, 256);                               // (the arrays are free again)
             }
-            const float ratio = sigma > 0.0f ? sc * (kBoost / sigma) : sc;   // (sigma 0: every finite scale is 0)
             if (i >= L::kPBufs)                                   // P(i - kPBufs) has been read
                 wait(kTbDone + ((i - L::kPBufs) & 1), (i - L::kPBufs) >> 1);
             unsigned char *line = smem + L::kP + (i % L::kPBufs) * L::kPBytes + (j >> 3) * kLboP + (c0 >> 3) * 128 + (j & 7) * 16;
 #pragma unroll
             for (int g = 0; g < V / 8; g++) {
                 uint32_t p4[4];
+                if constexpr (!kEarly) load_over(8 * g, 8);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     const float p0 = exp2_approx(x[8 * g + e]), p1 = exp2_approx(x[8 * g + e + 1]);
                     l[8 * g + e] += p0;
                     l[8 * g + e + 1] += p1;
-                    p4[e >> 1] = f16x2_rn(p0 * ratio, p1 * ratio);
-                    if (drafts) {   // a draft that the node does not see may have any scale
-                        if (x[8 * g + e] == -INFINITY) p4[e >> 1] &= 0xffff0000u;
-                        if (x[8 * g + e + 1] == -INFINITY) p4[e >> 1] &= 0x0000ffffu;
-                    }
+                    p4[e >> 1] = f16x2_rn(p0 * over[8 * g + e], p1 * over[8 * g + e + 1]);
                 }
                 if (lane < 16) *reinterpret_cast<uint4 *>(line + g * 128) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
             }
@@ -480,6 +505,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             if (lane == 0) tc::mbar_arrive(bar(kTbP + buf));
         }
         // the sums of the query rows, and what their accumulators are multiplied by
+        named_sync(1, 256);                                       // (the arrays are free)
         const float bl = butterfly<V, false>(l);
         if ((lane & kLow) == 0) red[quad * NQ + c0 + ((lane >> kShift) & (V - 1))] = bl;
         named_sync(1, 256);
@@ -487,15 +513,14 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             const float sum = (red[tid] + red[NQ + tid]) + (red[2 * NQ + tid] + red[3 * NQ + tid]);
             const bool none = tid >= live || sum == 0.0f;         // (a node past the tree's, or no visible key)
             // (scores that are all NaN set no reference: theirs is 0)
-            const float m = fac[tid].y == kTrNone ? 0.0f : fac[tid].y * 0.6931471805599453f;
-            const float scale = sigma * (1.0f / kBoost);
-            alpha[tid] = none ? -1.0f : (direct ? scale / sum : scale);   // (-1: not a factor)
+            const float ref = fac[tid].y, sigma = 1.0f / inv[tid];
+            alpha[tid] = none ? -1.0f : (direct ? sigma / sum : sigma * kUnhead);   // (-1: not a factor)
             if (orow[tid] >= 0) {
                 if (!direct) {
-                    part_ml[2 * orow[tid]] = none ? -INFINITY : m;
-                    part_ml[2 * orow[tid] + 1] = none ? 0.0f : sum;
+                    part_ml[2 * orow[tid]] = none ? -INFINITY : ref + kHead;
+                    part_ml[2 * orow[tid] + 1] = none ? 0.0f : sum * kUnhead;
                 } else if (a.lse) {
-                    a.lse[orow[tid]] = none ? -INFINITY : m + logf(sum);
+                    a.lse[orow[tid]] = none ? -INFINITY : ref * 0.6931471805599453f + logf(sum);
                 }
             }
         }

@@ -10,9 +10,15 @@ namespace glm {
 namespace tree {
 
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr float kGrow = 12.0f;                 // a score passes its reference by at most 2^12
-constexpr float kSpread = 2.0f;                // a row scale is at most 2 sigma
-constexpr float kBoost = 4.0f;                 // P' <= 2^12 * 2 * 4 = 2^15 < 65504
+// The softmax weights of a query row. It keeps a reference ref and log2 sigma, whole numbers in log2 units:
+// p = 2^(s - ref) goes to the sum, P' = p scale / sigma as fp16 to the product with the codes. When they are set,
+// from the keys that the row sees, the largest p and the largest P' are at most 2^kHead and above half of that;
+// they move when a P' would pass fp16's range, so that rescales are rare and, by powers of two, exact. A
+// row's sigma is its own, and follows what its keys weigh times their scale: a large scale in a key that
+// the row does not see, or that weighs nothing, costs the others none of fp16's range.
+constexpr float kHead = 2.0f, kUnhead = 0x1p-2f;   // (2^-kHead)
+constexpr float kTop = 15.9f;                  // log2 of the largest P' (fp16: 65,504)
+constexpr float kFltMax = 3.402823466e38f;
 
 // The keys of a sequence: those of the index list, then the drafted rows, in tiles. The lengths as they are
 // in memory are asked for first of all in a kernel and used as late as can be.
@@ -312,12 +318,31 @@ __device__ __forceinline__ float finite_max(float v) {
 }
 // The power of two that puts a bf16 magnitude (its bits) in [2^14, 2^15): bf16 values so scaled are
 // exact in fp16 (those below 2^-17 of the range aside).
-// sigma for a largest scale: the power of two at or above it, and such that kBoost / sigma is finite.
-__device__ __forceinline__ float sigma_of(float smax) { return fmaxf(pow2_ceil(smax), 0x1p-125f); }
 __device__ __forceinline__ int query_exponent(unsigned bits) {
     return bits == 0u ? 0 : min(120, max(-120, 14 - (static_cast<int>(bits >> 7) - 127)));
 }
 __device__ __forceinline__ float pow2f_exact(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// 2^d of a whole number d <= 127; 0 below -126.
+__device__ __forceinline__ float pow2_whole(float d) { return d < -126.0f ? 0.0f : pow2f_exact(static_cast<int>(d)); }
+// A query row's reference and log2 sigma, [-126, 126].
+struct Scaling {
+    float ref, log_sigma;
+    bool none;                                 // it has seen no key
+};
+// They move for a tile whose largest score is x and whose largest score plus log2 scale is y, less the reference (-infinity: no
+// key that the row sees, or scores that are NaN). What the sum so far has to be multiplied by, and the output.
+__device__ __forceinline__ void move_scaling(Scaling &s, float x, float y, float &l_factor, float &o_factor) {
+    l_factor = o_factor = 1.0f;
+    if (!(x > -INFINITY)) return;
+    const float ref = s.none || x > kHead ? s.ref + ceilf(x - kHead) : s.ref, delta = s.ref == ref ? 0.0f : ref - s.ref;
+    float sigma = fminf(fmaxf(ceilf(y - delta - kHead), -126.0f), 126.0f);
+    if (!s.none) {
+        sigma = delta == 0.0f && y - s.log_sigma <= kTop ? s.log_sigma : fmaxf(s.log_sigma - delta, sigma);
+        l_factor = pow2_whole(-delta);
+        o_factor = pow2_whole(s.log_sigma - sigma - delta);
+    }
+    s = {ref, sigma, false};
+}
 // 8 bf16 values times f as 8 fp16 values.
 __device__ __forceinline__ uint4 bf16_to_f16x8(const uint4 &v, float f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -61,14 +61,15 @@ struct PrLayout {
     static constexpr int kMax = kScl + kPrMeta * kPrKeys * 4;    // [3][8] largest finite scale of a K warp's keys (6 used)
     static constexpr int kValid = kMax + kPrMeta * 8 * 4;       // [3][96] bytes: 1 where there is a key
     static constexpr int kFull = kValid + kPrMeta * kPrKeys;     // [3][2][8] bytes: 1 where a K warp's keys are all there
-    static constexpr int kRed = kFull + kPrMeta * 16;            // [2][64]
-    static constexpr int kRowK = kRed + 128 * 4;                 // [64] score factors
+    static constexpr int kLog = kFull + kPrMeta * 16;            // [3][96] log2 of the row scales
+    static constexpr int kRed = kLog + kPrMeta * kPrKeys * 4;    // [2][64] pairs
+    static constexpr int kRowK = kRed + 128 * 8;                 // [64] score factors
     static constexpr int kBar = kRowK + kPrRows * 4;
     static constexpr int kTmem = kBar + kPbCount * 8;
     static constexpr int kBytes = kTmem + 8;
     static constexpr int kAlloc = kBytes + 1024;                 // from a 1024-byte aligned base
     static_assert(kPrRows == 16 * kPrSoft, "query rows of a softmax warp");
-    static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 8 == 0 && kFull % 16 == 0 && kMax % 16 == 0 && kK % 1024 == 0 &&
+    static_assert(kBar % 8 == 0 && kScl % 16 == 0 && kValid % 8 == 0 && kFull % 16 == 0 && kLog % 16 == 0 && kMax % 16 == 0 && kK % 1024 == 0 &&
                       kV % 1024 == 0 && kKBlock % 1024 == 0 && kVBlock % 1024 == 0 && kRawK % 128 == 0 && kRawV % 128 == 0, "alignment");
     static_assert(kAlloc <= 232448 && kPrRows * kPartRow <= kP, "shared memory of one CTA");
 };
@@ -121,6 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     float *scl = reinterpret_cast<float *>(smem + L::kScl);
+    float *slog = reinterpret_cast<float *>(smem + L::kLog);
     float *smx = reinterpret_cast<float *>(smem + L::kMax);
     uint8_t *val = smem + L::kValid, *full = smem + L::kFull;
     float *red = reinterpret_cast<float *>(smem + L::kRed);
@@ -301,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 for (int h = 0; h < 2; h++)
                     v[r][h] = R::line(codes + r * R::kCodes, tails + r * R::kTail, lane + 32 * h, lane / 2 + 16 * h);
             const unsigned bits = __ballot_sync(0xffffffffu, rows != -1);
-            const float mx = finite_max(holds ? sc : 0.0f);
+            const float mx = finite_max(holds ? sc : 0.0f), lg = __log2f(sc);
             // the next rows, into the slots just read
             const int nxt = row_of(t + 1, my_key, e1);
             if (i + 1 < n_tiles) R::template fetch<kN>(codes, tails, a, nxt, 0, has_drafts(t + 1));
@@ -311,6 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             else start();
             if (holds) {
                 scl[m * kPrKeys + my_key] = sc + (sc - sc);   // (an infinite scale: NaN, as 0 codes times it are)
+                slog[m * kPrKeys + my_key] = lg;
                 val[m * kPrKeys + my_key] = rows != -1 ? 1 : 0;
             }
             if (lane == 0) {
@@ -422,13 +425,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         const int r = r0 + row;
         const float qk = rowk[row];
         const uint64_t seen = r < live ? a.mask[static_cast<int64_t>(b) * a.n_nodes + r / H] : 0ull;
-        float ref = 0.0f, l = 0.0f, sigma = 0.0f;
-        bool none = true;                                               // the row has seen no key
-        float *mine = red + half * 64 + row, *other = red + (1 - half) * 64 + row;   // two threads share a row
+        Scaling scaling{0.0f, 0.0f, true};
+        float l = 0.0f, inv = 1.0f;                                     // (1 / sigma)
+        const int mine = half * 64 + row, other = (1 - half) * 64 + row;   // two threads share a row
+        float2 *red2 = reinterpret_cast<float2 *>(red);
         unsigned char *prow = smem + L::kP + (row >> 3) * L::kPGroup + key0 * 16 + (row & 7) * 16;
         for (int i = 0; i < n_tiles; i++) {
             const int t = t0 + i, m = i % kPrMeta;
             wait(kPbMeta + m, i / kPrMeta);
+            // What a score may be: its p at most 2^kTop, and its product with any scale of the tile (of all keys, seen or
+            // not) at most 2^kTop sigma; of a row without a reference: none.
+            const float4 ma = *reinterpret_cast<const float4 *>(smx + m * 8), mb = *reinterpret_cast<const float4 *>(smx + m * 8 + 4);
+            const float smax = fmaxf(max3(ma.x, ma.y, max3(ma.z, ma.w, mb.x)), max3(mb.y, mb.z, mb.w));
+            const int bits = max(0, static_cast<int>(__float_as_uint(smax * inv) >> 23) - 126);   // smax / sigma < 2^bits
+            const float most = scaling.none ? -INFINITY : kTop - static_cast<float>(bits);
             wait(kPbS + (i & 1), i >> 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
@@ -442,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive_leader(bar(kPbSFree + (i & 1)));
-                const uint64_t qk2 = pack2(qk, qk), ref2 = pack2(-ref, -ref);
+                const uint64_t qk2 = pack2(qk, qk), ref2 = pack2(-scaling.ref, -scaling.ref);
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e += 4) {
                     const ulonglong2 s = sc4[e >> 2];
@@ -452,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 }
             }
             const uint2 fw = *reinterpret_cast<const uint2 *>(full + m * 16 + half * 8);
-            const bool partial = (fw.x & fw.y) != 0x01010101u || has_drafts(t);
+            bool partial = (fw.x & fw.y) != 0x01010101u || has_drafts(t);
             uint64_t keys = (1ull << kPrHalf) - 1;                      // this thread's keys
             if (partial) {
                 const uint2 *vb = reinterpret_cast<const uint2 *>(val + m * kPrKeys + key0);
@@ -474,47 +484,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < kPrHalf; e += 2) mx = max3(mx, x[e], x[e + 1]);
-            const float4 ma = *reinterpret_cast<const float4 *>(smx + m * 8), mb = *reinterpret_cast<const float4 *>(smx + m * 8 + 4);
-            const float smax = fmaxf(max3(ma.x, ma.y, max3(ma.z, ma.w, mb.x)), max3(mb.y, mb.z, mb.w));
-            const bool over = none ? mx > -INFINITY : mx > kGrow;
-            const bool grow = smax > kSpread * sigma;                   // (sigma 0: no scale yet)
-            if (named_or(1, 32 * kPrSoft, over) || grow) {
-                // the references and sigma move; what they scale is rescaled
-                *mine = mx;
-                const float sig_new = grow ? sigma_of(smax) : sigma;
-                const float beta = sigma == 0.0f ? 1.0f : sigma / sig_new;   // powers of two: exact
-                sigma = sig_new;
+            if (named_or(1, 32 * kPrSoft, mx > most)) {
+                // the scaling of the rows moves, where it has to, and what it scales is rescaled
+                float my = -INFINITY;
+                const float4 *lg4 = reinterpret_cast<const float4 *>(slog + m * kPrKeys + key0);
+#pragma unroll
+                for (int e = 0; e < kPrHalf; e += 4) {
+                    const float4 lg = lg4[e >> 2];
+                    my = max3(max3(my, x[e] + lg.x, x[e + 1] + lg.y), x[e + 2] + lg.z, x[e + 3] + lg.w);
+                }
+                red2[mine] = make_float2(mx, my);
                 named_sync(1, 32 * kPrSoft);
-                const float mr = fmaxf(mx, *other);
-                const float delta = mr > (none ? -INFINITY : kGrow) ? mr : 0.0f;
-                const float alpha = none ? 0.0f : exp2f(-delta);
-                none = none && !(mr > -INFINITY);
-                ref += delta;
-                l *= alpha;
+                const float2 o = red2[other];
+                const float old = scaling.ref;
+                float fl, fo;
+                move_scaling(scaling, fmaxf(mx, o.x), fmaxf(my, o.y), fl, fo);
+                inv = pow2f_exact(-static_cast<int>(scaling.log_sigma));
+                l *= fl;
+                const float delta = scaling.ref == old ? 0.0f : scaling.ref - old;
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e++) x[e] -= delta;
-                if (i > 0) {
+                if (i > 0 && __any_sync(0xffffffffu, fo != 1.0f)) {
                     wait(kPbDone + ((i - 1) & 1), (i - 1) >> 1);
                     ok = __all_sync(0xffffffffu, ok);
                     tc::fence_after_sync();
-                    const float f = alpha * beta;
-                    if (__any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 32) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(tmem + lanes + c, o);
-                            tc::tmem_wait_ld();
+                    for (int c = 0; c < 256; c += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(tmem + lanes + c, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::tmem_st32(tmem + lanes + c, o);
-                        }
-                        tc::tmem_wait_st();
+                        for (int e = 0; e < 32; e++) v[e] = __float_as_uint(__uint_as_float(v[e]) * fo);
+                        tc::tmem_st32(tmem + lanes + c, v);
                     }
+                    tc::tmem_wait_st();
                     tc::fence_before_sync();
                 }
-                named_sync(1, 32 * kPrSoft);                            // (red is free again)
             }
-            const float inv = sigma > 0.0f ? kBoost / sigma : 1.0f;     // (sigma 0: every finite scale is 0)
+            if (!(smax * inv <= kFltMax)) {   // keys whose scale over sigma is not finite weigh nothing
+                partial = true;
+#pragma unroll 1
+                for (int e = 0; e < kPrHalf; e++)
+                    if (!(scl[m * kPrKeys + key0 + e] * inv <= kFltMax)) keys &= ~(1ull << e);
+            }
             uint32_t p[kPrHalf / 2];
             const uint64_t inv2 = pack2(inv, inv);
             uint64_t l2[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
@@ -552,23 +564,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             if (lane == 0) arrive_leader(bar(kPbP));
         }
         // the row's sum over its two threads
-        *mine = l;
+        named_sync(1, 32 * kPrSoft);                                    // (red is free)
+        red[mine] = l;
         named_sync(1, 32 * kPrSoft);
-        l += *other;
+        l += red[other];
         named_sync(1, 32 * kPrSoft);
+        const float sigma = 1.0f / inv;
         const bool empty = r >= live || l == 0.0f;
-        const float scale = sigma * (1.0f / kBoost);
         if (key0 == 0) {
-            red[row] = empty ? 0.0f : (direct ? scale / l : scale);
+            red[row] = empty ? 0.0f : (direct ? sigma / l : sigma * kUnhead);
             red[64 + row] = empty ? 0.0f : 1.0f;
             if (r < n_rows_q) {
                 const int64_t o = row_at(r);
-                const float mn = ref * 0.6931471805599453f;
                 if (!direct) {
-                    part_ml[2 * o] = empty ? -INFINITY : mn;
-                    part_ml[2 * o + 1] = empty ? 0.0f : l;
+                    part_ml[2 * o] = empty ? -INFINITY : scaling.ref + kHead;
+                    part_ml[2 * o + 1] = empty ? 0.0f : l * kUnhead;
                 } else if (a.lse) {
-                    a.lse[o] = empty ? -INFINITY : mn + logf(l);
+                    a.lse[o] = empty ? -INFINITY : scaling.ref * 0.6931471805599453f + logf(l);
                 }
             }
         }

@@ -1,0 +1,96 @@
+"""The softmax weights of the tree attention: a node's output depends on the rows that it sees, each by what it weighs.
+
+Rows that a node does not see, and rows that it sees but that weigh nothing, may have scales far above the others',
+without an effect on its output. Errors allowed: those of tests/tree_bounds.py, from the rows seen alone."""
+import numpy as np
+import pytest
+
+import synth
+from tests import tree_bounds as B
+from tests import tree_reference as R
+from tests.test_gpu_tree import SM, case, launch
+from tests.test_gpu_tree_edges import set_scale
+
+pytestmark = pytest.mark.gpu
+
+FLT_MAX = float(np.finfo(np.float32).max)
+
+# (batch, nodes, heads, width): the kernels' tiles of 16, 32, 64 and 128 query rows, one run of keys or several
+CUTS = [(2, 6, 4, 70), (8, 6, 4, 700), (4, 6, 10, 700), (150, 6, 10, 70), (2, 6, 40, 70), (2, 6, 40, 1500)]
+
+
+def check(c, out, lse, nodes=None, sm=SM):
+    """The nodes (None: all) of a call's first two and last sequences against the bounds."""
+    o, l = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    q = synth.bf16_bits_to_f32(c["q"]).astype(np.float64)
+    for b, i, want, wl, tol, ltol in B.tree(c, sm, q, sorted({0, 1, len(q) - 1} & set(range(len(q))))):
+        if nodes is not None and i not in nodes:
+            continue
+        if np.isneginf(wl).all():
+            assert np.isneginf(l[b, i]).all() and not o[b, i].any(), (b, i)
+            continue
+        err = np.abs(o[b, i] - want)
+        assert (err <= tol).all(), (b, i, float((err / tol).max()), float(err.max()))
+        assert (np.abs(l[b, i] - wl) <= ltol).all(), (b, i, float((np.abs(l[b, i] - wl) / ltol).max()))
+
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+def test_random_rows(cuda, fmt, cut):
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width)
+    c = case(rng, fmt, b, T, H, width, [width - i % 60 for i in range(b)], [T - i % 3 for i in range(b)], n_rows=700, holes=0.05)
+    check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("value", [2.0 ** 16, 2.0 ** 30, 1e30, FLT_MAX])
+def test_drafts_that_a_node_does_not_see(cuda, fmt, cut, value):
+    # drafts 1 and 4 hold scales of any finite size; node 5 is padding of the tree, with no bit set anywhere
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 1)
+    c = case(rng, fmt, b, T, H, width, [width - i % 60 for i in range(b)], [T] * b, n_rows=700)
+    for s in range(b):
+        set_scale(c["draft"], [s * T + 1, s * T + 4, s * T + 5], fmt, value)
+    c["masks"] = [[0b000001, 0b000010, 0b000101, 0b001001, 0b011001, 0]] * b
+    check(c, *launch(c, cuda), nodes=(0, 2, 3, 5))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 20, 2.0 ** 100])
+@pytest.mark.parametrize("first", [True, False])
+def test_rows_that_are_seen_and_weigh_nothing(cuda, fmt, cut, ratio, first):
+    # a row of the list far above the others in scale and far below them in score, at the start or the middle of it
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 2)
+    c = case(rng, fmt, b, T, H, width, [width] * b, [T] * b, n_rows=700)
+    q = synth.bf16_bits_to_f32(c["q"]) + np.float32(0.5)          # (a positive sum over the dims, so that ...)
+    c["q"] = synth.f32_to_bf16_bits(q)
+    raw = c["cache"].view(np.uint8)
+    raw[7, :288 if fmt == "fp4" else 512] = {"int8": 0x9C, "fp8": 0xFE, "fp4": 0xAA}[fmt]       # (... -100, -448, -1 give a low score)
+    if fmt == "fp4":
+        raw[7, 256:288] = 0x7E                                   # (block scales of 448)
+    typical = float(np.median(R.row_scales(c["cache"], np.arange(700), fmt)))
+    c["rows"][c["rows"] == 7] = 8
+    c["rows"][:, 0 if first else width // 2] = 7
+    set_scale(c["cache"], [7], fmt, typical * ratio)
+    s = R.values(c["cache"], [7], fmt)[0] @ synth.bf16_bits_to_f32(c["q"]).astype(np.float64).reshape(-1, 512).T * SM
+    assert s.max() < -150.0                                       # (far below any other row's)
+    check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("order", [1, -1])
+def test_scales_and_scores_that_move_against_each_other(cuda, fmt, cut, order):
+    # scales from 2^-12 to 2^6 of the usual along the list, queries so large that the scores move with them
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 3)
+    c = case(rng, fmt, b, T, H, width, [width] * b, [T] * b, n_rows=700, q_scale=4.0)
+    sc = R.row_scales(c["cache"], np.arange(700), fmt)
+    set_scale(c["cache"], np.arange(700), fmt, (sc * 2.0 ** np.linspace(-12, 6, 700)).astype(np.float32))
+    c["rows"] = np.sort(c["rows"], axis=1)[:, ::order].copy()
+    check(c, *launch(c, cuda))
