@@ -16,7 +16,12 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 // they move when a P' would pass fp16's range, so that rescales are rare and, by powers of two, exact. A
 // row's sigma is its own, and follows what its keys weigh times their scale: a large scale in a key that
 // the row does not see, or that weighs nothing, costs the others none of fp16's range.
-constexpr float kHead = 2.0f, kUnhead = 0x1p-2f;   // (2^-kHead)
+// kHead: fp16 has no bits below 2^-24, so a weight is off by at most 2^-24 - kHead of the row's largest (each times its
+// scale) beside its 2^-11; with 8, over 2^20 rows, that is 2^-12, an eighth of half a step of the bf16 output. Above
+// it there is room for scores that grow by 2^7.9. 8 nodes over 262,144 rows, us a call: 364 with 2, 371 with
+// 8 (338 and 341 one at a time: rescales cost next to nothing, bits that are not 0 take power); 373 and, with 10, 384
+// on another chip.
+constexpr float kHead = 8.0f, kUnhead = 0x1p-8f;   // (2^-kHead)
 constexpr float kTop = 15.9f;                  // log2 of the largest P' (fp16: 65,504)
 constexpr float kFltMax = 3.402823466e38f;
 

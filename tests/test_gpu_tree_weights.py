@@ -8,7 +8,7 @@ import pytest
 import synth
 from tests import tree_bounds as B
 from tests import tree_reference as R
-from tests.test_gpu_tree import SM, case, launch
+from tests.test_gpu_tree import SM, STORE, case, launch
 from tests.test_gpu_tree_edges import set_scale
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,30 @@ def test_scales_and_scores_that_move_against_each_other(cuda, fmt, cut, order):
     set_scale(c["cache"], np.arange(700), fmt, (sc * 2.0 ** np.linspace(-12, 6, 700)).astype(np.float32))
     c["rows"] = np.sort(c["rows"], axis=1)[:, ::order].copy()
     check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("H", [4, 20, 60, 80])
+def test_a_long_tail_far_below_the_peaks(cuda, fmt, H):
+    # 262,144 rows: in every 1,024 one row 12 to 20 nats above the others, which all weigh the same and alone hold
+    # values in the upper dims; one of them in 63 with a scale eight times the others'
+    n = 1 << 18
+    x = np.zeros((64, 512), np.float32)
+    x[0, :256] = 1.0
+    x[1:, 256:] = 1.0 + np.arange(63)[:, None] / 64.0
+    x[63] *= 8.0
+    cache = np.zeros((64, R.ROW[fmt]), np.int8 if fmt == "int8" else np.uint8)
+    STORE[fmt](synth.f32_to_bf16_bits(x), np.arange(64, dtype=np.int64), cache)
+    rows = 1 + np.arange(n, dtype=np.int32) % 63
+    rows[::1024] = 0
+    gap = np.linspace(12.0, 20.0, H)
+    q = np.zeros((1, 1, H, 512), np.float32)
+    q[..., :256] = (gap / (256 * SM))[None, None, :, None]
+    c = dict(fmt=fmt, cache=cache, draft=cache[:1], rows=rows[None], row_len=np.array([n], np.int32),
+             n_tree=np.array([1], np.int32), masks=[[0]], q=synth.f32_to_bf16_bits(q))
+    out, lse = launch(c, cuda)
+    want, wl, tol, ltol = B.node(synth.bf16_bits_to_f32(c["q"])[0, 0].astype(np.float64), R.values(cache, np.arange(64), fmt),
+                                 R.row_scales(cache, np.arange(64), fmt), SM, times=np.bincount(rows, minlength=64))
+    err = np.abs(out[0, 0].float().cpu().numpy().astype(np.float64) - want)
+    assert (err <= tol).all(), float((err / tol).max())
+    assert (np.abs(lse[0, 0].cpu().numpy() - wl) <= ltol).all()

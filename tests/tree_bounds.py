@@ -18,7 +18,7 @@ import numpy as np
 
 from tests.tree_reference import U32, row_scales, values
 
-FLUSH = 2.0 ** -26                                     # G = 2
+FLUSH = 2.0 ** -32                                     # G = 8
 
 
 def node(q, c, scales, sm_scale, times=None):
