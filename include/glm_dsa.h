@@ -548,6 +548,13 @@ int glm_lse_merge(const glm_dsa_dims *dims, const float *out_parts_dev, const fl
  */
 #define GLM_CROSS_CTA_WAIT_LIMIT (1u << 21)
 int glm_debug_set_cross_cta_wait_limit(uint32_t polls);
+/*
+ * on != 0: in calls of glm_tree_mla_decode, _fp8 and _fp4 made from then on by this process, every wait inside a CTA
+ * or a pair gives up at once, as one does after 2^22 polls (the wait for its last product is made all the same).
+ * A test checks the give-up path with it without a fault: the kernel sets bit 32 or 64 of the status word and
+ * leaves outputs that mean nothing. 0 restores the default. Returns GLM_OK.
+ */
+int glm_debug_tree_waits_give_up(int32_t on);
 
 /* ------------------------------------------------------------------------------------------ */
 /* the whole decode step in one call                                                           */

@@ -50,7 +50,7 @@ EXPORTS = ("glm_check_dims", "glm_status_string", "glm_last_cuda_error", "glm_kv
            "glm_debug_set_cross_cta_wait_limit", "glm_mla_v_up", "glm_cp_candidates", "glm_merge_topk",
            "glm_lse_merge", "glm_kv_store_fp4", "glm_sparse_mla_decode_fp4", "glm_dsa_step_plan",
            "glm_tree_mla_decode", "glm_tree_mla_decode_fp8", "glm_tree_mla_decode_fp4", "glm_block_tables",
-           "glm_tree_commit")
+           "glm_tree_commit", "glm_debug_tree_waits_give_up")
 
 
 class glm_dsa_dims(C.Structure):
@@ -638,6 +638,15 @@ def _tree_mla(fn, name, dims, q, cache, rows, draft, mask, sm_scale, out, worksp
         raise ValueError(f"draft must hold {B * T} rows of {row_bytes} bytes, got {draft.numel()} bytes")
     _call(fn, name, dev, stream, C.byref(dims), p[0], p[1], cache.numel() // row_bytes, p[2], p[3], width, p[4], p[5], p[6], B,
           T, sm_scale, p[7], p[8], p[9], ws_bytes)
+
+
+lib.glm_debug_tree_waits_give_up.argtypes = [_I32]
+lib.glm_debug_tree_waits_give_up.restype = C.c_int
+
+
+def glm_debug_tree_waits_give_up(on: bool) -> None:
+    """Whether every wait of the tree attention gives up at once, in calls made from then on (tests only)."""
+    _check(lib.glm_debug_tree_waits_give_up(1 if on else 0), "glm_debug_tree_waits_give_up")
 
 
 def glm_tree_mla_decode(dims, q, cache, rows, draft, mask, sm_scale, out, workspace, lse=None, row_len=None,

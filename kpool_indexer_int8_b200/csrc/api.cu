@@ -1,5 +1,6 @@
 // api.cu -- the C ABI (include/glm_dsa.h): host-side argument checks, workspace sizing and the
 // kernel launches of each entry point. Nothing is enqueued unless every check passes.
+#include <atomic>
 #include <cstdint>
 
 #include "block_tables.cuh"
@@ -10,6 +11,7 @@
 
 namespace {
 thread_local int g_last_cuda_error = 0;
+std::atomic<bool> g_tree_waits_give_up{false};
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 }  // namespace
 
@@ -217,6 +219,11 @@ int glm_last_cuda_error(void) { return g_last_cuda_error; }
 
 int glm_debug_set_cross_cta_wait_limit(uint32_t polls) {
     return cuda_status(glm::set_cross_cta_wait_limit(polls));
+}
+
+int glm_debug_tree_waits_give_up(int32_t on) {
+    g_tree_waits_give_up.store(on != 0, std::memory_order_relaxed);
+    return GLM_OK;
 }
 
 int glm_kv_store_int8(const glm_dsa_dims *dims, const void *latent, const int64_t *slots,
@@ -652,6 +659,7 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     a.status = reinterpret_cast<int *>(ws + mla_acc_bytes(partials) + mla_ml_bytes(partials));
+    a.give_up = g_tree_waits_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const glm::TreePlan plan = glm::tree_plan(batch, n_nodes, H, width, sms);
     rc = cuda_status(glm::launch_tree_mla(plan, a, format, part_acc, part_ml, st));

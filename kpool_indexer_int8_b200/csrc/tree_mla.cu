@@ -42,7 +42,7 @@ using namespace tree;
 constexpr int kTrSoft = 8;                     // warps 0-7 softmax, then the widening warps and one for the tensor cores
 constexpr int kTrKeys = 64;                    // keys of a tile
 
-enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbCount = 10 };
+enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbEnd = 10, kTbCount };
 
 template <int NQ>
 struct TrLayout {
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tc::mbar_init(bar(kTbSFree + i), 8);
                 tc::mbar_init(bar(kTbP + i), 8);
             }
+            tc::mbar_init(bar(kTbEnd), 1);
             tc::mbar_fence_init();
         }
     }
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     // a wait that gives up marks the thread, which skips its later waits; the output is then NaN
-    bool ok = true;
+    bool ok = !a.give_up;
     auto wait = [&](int i, int use) {
         if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
     };
@@ -349,6 +350,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             if (i > 0 && !early) accumulate(i - 1);
         }
         accumulate(n_tiles - 1);
+        if (tc::elect_one()) tc::mma_commit(bar(kTbEnd));
+        __syncwarp();
     } else {
         // ---------------- softmax ----------------
         const int quad = warp & 3, hh = warp >> 2, c0 = hh * V;
@@ -525,13 +528,11 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             }
         }
     }
-    wait(kTbDone + ((n_tiles - 1) & 1), (n_tiles - 1) >> 1);      // every product is done
+    // Every product is done. (A barrier of its own, used once: that of a tile says nothing to a thread that
+    // gave up, whose products may be several phases behind.)
+    if (!tc::mbar_wait(bar(kTbEnd), 0, kWaitLimit)) ok = false;
     const bool all_ok = __syncthreads_and(ok);
-    if (!all_ok) {   // a wait gave up: the status word, and a bounded wait for products still in flight
-        if (tid == 0) atomicOr(a.status, 32);
-        tc::mbar_wait(bar(kTbDone + ((n_tiles - 1) & 1)), static_cast<uint32_t>(((n_tiles - 1) >> 1) & 1), kWaitLimit);
-        __syncthreads();
-    }
+    if (!all_ok && tid == 0) atomicOr(a.status, 32);
     tc::fence_after_sync();
     if (warp < 16) {
         // O^T: tile mt of 128 latent dims, lane quadrant warp % 4 (dim 128 mt + 32 quad + lane); rows of the

@@ -26,6 +26,7 @@ struct TreeArgs {
     uint16_t *out;                  // bf16 [batch][n_nodes][n_heads][512]
     float *lse;                     // [batch][n_nodes][n_heads] or null
     int *status;
+    bool give_up;                   // a test: every wait but the last gives up at once
 };
 
 // How a call is cut: query rows (node, head) in tiles of `nq` (128: the two-CTA kernel), the keys of

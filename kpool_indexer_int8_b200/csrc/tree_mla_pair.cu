@@ -44,7 +44,7 @@ constexpr int kPrMeta = 3;                     // tiles whose scales are kept
 constexpr uint32_t kPrSCol = 256;              // two score accumulators of 48 columns after the output's 256
 constexpr uint32_t kPrSStep = 64;
 
-enum PrBar { kPbK = 0, kPbV, kPbP, kPbSFree, kPbS = 5, kPbDone = 7, kPbMeta = 9, kPbCount = 12 };
+enum PrBar { kPbK = 0, kPbV, kPbP, kPbSFree, kPbS = 5, kPbDone = 7, kPbMeta = 9, kPbEnd = 12, kPbCount };
 
 struct PrLayout {
     static constexpr int kQ = 0;                                 // 8 row groups x 64 dim groups x 128 B
@@ -227,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 tc::mbar_init(bar(kPbDone + i), 1);
             }
             for (int i = 0; i < kPrMeta; i++) tc::mbar_init(bar(kPbMeta + i), kPrK);
+            tc::mbar_init(bar(kPbEnd), 1);
             tc::mbar_fence_init();
         }
     }
@@ -239,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
         tc::fence_after_sync();
         tmem = *tmem_slot;
     };
-    bool ok = true;
+    bool ok = !a.give_up;
     auto wait = [&](int i, int use) {
         if (ok && !tc::mbar_wait(bar(i), static_cast<uint32_t>(use & 1), kWaitLimit)) ok = false;
     };
@@ -414,6 +415,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 if (i > 0) accumulate(i - 1);
             }
             accumulate(n_tiles - 1);
+            if (tc::elect_one()) commit_pair(bar(kPbEnd));
+            __syncwarp();
         }
     } else {
         // ---------------- softmax ----------------
@@ -585,14 +588,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             }
         }
     }
-    // every product of the pair is done: the output
-    wait(kPbDone + ((n_tiles - 1) & 1), (n_tiles - 1) >> 1);
+    // Every product of the pair is done: the output. (A barrier of its own, used once and told to both CTAs: that of
+    // a tile says nothing to a thread that gave up, whose products may be several phases behind.)
+    if (!tc::mbar_wait(bar(kPbEnd), 0, kWaitLimit)) ok = false;
     const bool all_ok = __syncthreads_and(ok);
-    if (!all_ok) {   // a wait gave up: the status word, and a bounded wait for products still in flight
-        if (tid == 0) atomicOr(a.status, 64);
-        tc::mbar_wait(bar(kPbDone + ((n_tiles - 1) & 1)), static_cast<uint32_t>(((n_tiles - 1) >> 1) & 1), kWaitLimit);
-        __syncthreads();
-    }
+    if (!all_ok && tid == 0) atomicOr(a.status, 64);
     tc::fence_after_sync();
     // the output or partials go through shared memory (over Q, K and V, which no product reads any more;
     // rows 16 bytes apart in the banks), then, whole lines of them,
