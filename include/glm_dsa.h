@@ -419,8 +419,9 @@ int glm_mla_v_up(const glm_dsa_dims *dims, const void *o_lat_dev, const void *w_
  *   mask_dev    uint64 [batch, n_nodes];  n_tree_dev int32 [batch] or NULL (= n_nodes), clamped
  *   out_dev     bf16 like q_dev;  lse_dev fp32 [batch, n_nodes, n_heads] or NULL
  *   workspace_dev / ws_bytes: >= glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width),
- *               256-byte aligned. Its last 256 bytes start with a status word set nonzero if a wait
- *               on the tensor cores gave up (outputs then invalid; never cleared by the library).
+ *               256-byte aligned. The last 256 bytes of ws_bytes (rounded down to a multiple of 256) start with
+ *               a status word set nonzero if a wait on the tensor cores gave up (outputs then invalid; never
+ *               cleared by the library): of every call with this workspace, whatever its shape.
  *               Calls that may run at the same time (other streams, graphs) need workspaces of their own.
  * out must not overlap q (refused) nor any other input. 1 <= n_nodes <= 64, 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with
  * mask 1 is an ordinary decode token whose own row is not in the cache yet. A row that a node does

@@ -658,7 +658,7 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
     a.sm_scale = sm_scale;
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
-    a.status = reinterpret_cast<int *>(ws + mla_acc_bytes(partials) + mla_ml_bytes(partials));
+    a.status = reinterpret_cast<int *>(ws + ws_bytes / 256 * 256 - 256);   // (the workspace's end, not what this call needs)
     a.give_up = g_tree_waits_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const glm::TreePlan plan = glm::tree_plan(batch, n_nodes, H, width, sms);

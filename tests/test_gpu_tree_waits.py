@@ -37,3 +37,31 @@ def test_waits_give_up_with_a_status_and_no_fault(cuda, fmt, B, T, H, width, bit
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     check(c, d["out"], d["lse"])
+
+
+def test_the_status_word_is_at_the_end_of_a_larger_workspace(cuda):
+    # one workspace for calls of different shapes: their status words are one, and no call's partials lie over it
+    big = case(np.random.default_rng(1), "int8", 2, 4, 64, 3000, [3000] * 2, [4] * 2, n_rows=400)
+    small = case(np.random.default_rng(2), "int8", 1, 2, 8, 300, [300], [2], n_rows=400)
+    b, s = device_args(big, cuda, kp.make_dims(64)), device_args(small, cuda, kp.make_dims(8))
+    n = b["workspace"].numel()
+    assert s["workspace"].numel() < n - 256
+    for extra in (0, 100):                                        # (a size that is no multiple of 256 too)
+        ws = torch.full((n + extra,), 0xFF, dtype=torch.uint8, device=cuda)
+        status = ws[n - 256:n - 252].view(torch.int32)
+        status.zero_()
+        b["workspace"] = s["workspace"] = ws
+        try:
+            kp.glm_debug_tree_waits_give_up(True)
+            CALL["int8"](kp.make_dims(8), **s)
+            torch.cuda.synchronize()
+        finally:
+            kp.glm_debug_tree_waits_give_up(False)
+        assert int(status.item()) == 32
+        status.zero_()
+        CALL["int8"](kp.make_dims(64), **b)
+        CALL["int8"](kp.make_dims(8), **s)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        check(big, b["out"], b["lse"])
+        check(small, s["out"], s["lse"])
