@@ -620,13 +620,15 @@ TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms) 
 }
 
 size_t tree_partials(int batch, int n_nodes, int n_heads, int width, int num_sms) {
-    // a plan of more than one part has at most 2 x 4 waves of runs of at most 128 query rows, plus
-    // one run a sequence
-    const long long rows = static_cast<long long>(batch) * n_nodes * n_heads;
-    long long tiles = tree_tiles(width, kTrKeys);
-    if (tiles > kTrMaxParts) tiles = kTrMaxParts;
-    const long long cap = 2ll * kTrLevels * num_sms * 128 + rows;
-    return static_cast<size_t>(rows * tiles < cap ? rows * tiles : cap);
+    // A plan of more than one part has at most as many runs as waves of its units, of nq query rows each (128 a pair
+    // of SMs is 64 an SM), and at most one for each tile. Every factor grows with the shape, or stays.
+    const long long rows = static_cast<long long>(n_nodes) * n_heads, all = tree_tiles(width, kTrKeys);
+    const long long tiles = all > kTrMaxParts ? kTrMaxParts : all;
+    const int nq = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    int waves = batch > 1 ? 2 : 1;
+    if (batch > 1 && batch * ((rows + 127) / 128) * all > 32ll * (num_sms / 2)) waves *= kTrLevels;
+    const long long cap = static_cast<long long>(waves) * num_sms * nq;
+    return static_cast<size_t>(batch * rows * tiles < cap ? batch * rows * tiles : cap);
 }
 
 cudaError_t launch_tree_mla(const TreePlan &p, const TreeArgs &a, int format, float *part_acc, float *part_ml,
