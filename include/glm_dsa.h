@@ -423,12 +423,13 @@ int glm_mla_v_up(const glm_dsa_dims *dims, const void *o_lat_dev, const void *w_
  *               a status word set nonzero if a wait on the tensor cores gave up (outputs then invalid; never
  *               cleared by the library): of every call with this workspace, whatever its shape.
  *               Calls that may run at the same time (other streams, graphs) need workspaces of their own.
- * out must not overlap q (refused) nor any other input. 1 <= n_nodes <= 64, 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with
- * mask 1 is an ordinary decode token whose own row is not in the cache yet. A row that a node does
- * not see has no effect on it, whatever it holds; a NaN or an infinite scale that it sees makes it NaN. The products run on the tensor cores with fp16
- * operands and fp32 accumulation: codes and (scaled by powers of two) queries exactly, a softmax
- * weight times its row's scale as one fp16 number (off by 2^-11 of itself, or 2^-32 of the largest that the query
- * row sees; glm_sparse_mla_decode carries 22 bits), sums and references in fp32.
+ * out, lse and the workspace must not overlap each other or an input (refused). 1 <= n_nodes <= 64,
+ * 0 <= width <= 1048576, batch * n_nodes <= 65535. A node of n_nodes = 1 with mask 1 is an ordinary decode token
+ * whose own row is not in the cache yet. A row that a node does not see has no effect on it, whatever it holds; a NaN
+ * or an infinite scale that it sees makes it NaN. The products run on the tensor cores with fp16 operands and fp32
+ * accumulation: codes and (scaled by powers of two) queries exactly, a softmax weight times its row's scale as one
+ * fp16 number (off by 2^-11 of itself, or 2^-32 of the largest that the query row sees; glm_sparse_mla_decode
+ * carries 22 bits), sums and references in fp32.
  */
 int glm_tree_mla_decode(const glm_dsa_dims *dims, const void *q_dev, const int8_t *cache_dev, int64_t n_rows,
                         const int32_t *rows_dev, const int32_t *row_len_dev, int32_t width,
@@ -494,7 +495,8 @@ int glm_block_tables(const int32_t *len_dev, const int32_t *n_new_dev, const int
  *   path_dev   int32 [batch, ld_path];  slots, q_seq, q_pos [n_cap], cu_new [batch + 1] as made
  *   draft_k, draft_gate  bf16 [batch, n_nodes, 128] and k, gate bf16 [batch, ld_tokens, 128], or all NULL
  * Tokens with a request, node, slot or position out of range (padding) copy nothing there. The
- * destinations must be distinct, and draft and cache must not overlap.
+ * destinations must be distinct. draft and cache must not overlap, nor draft_k or draft_gate and k or gate, nor cache, k
+ * and gate (refused).
  */
 int glm_tree_commit(const glm_dsa_dims *dims, const void *draft_dev, int32_t cache_format, const int32_t *path_dev,
                     int32_t batch, int32_t n_nodes, int64_t ld_path, const int64_t *slots_dev,

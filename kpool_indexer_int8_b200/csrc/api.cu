@@ -634,10 +634,20 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
         (lse && !aligned(lse, 4)))
         return GLM_ERR_INVALID_ARG;
     const int H = dims->n_heads, sms = num_sms();
-    const size_t q_bytes = static_cast<size_t>(batch) * n_nodes * H * glm::kLatent * 2;
-    if (overlap(q, q_bytes, out, q_bytes)) return GLM_ERR_INVALID_ARG;   // (CTAs read q while others write out)
     const size_t need = glm_dsa_workspace_size(dims, GLM_OP_TREE_MLA, batch, 0, n_nodes, width);
     if (workspace == nullptr || ws_bytes < need || !aligned(workspace, 256)) return GLM_ERR_WORKSPACE;
+    // no output may be an input or another output: CTAs read while others write
+    const size_t nodes = static_cast<size_t>(batch) * n_nodes, q_bytes = nodes * H * glm::kLatent * 2;
+    const size_t row_bytes = format == glm::kFmtFp4 ? glm::kFp4RowBytes : glm::kRowBytes, per_seq = static_cast<size_t>(batch) * 4;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } bufs[] = {{out, q_bytes}, {lse, nodes * H * 4}, {workspace, need}, {q, q_bytes}, {cache, static_cast<size_t>(n_rows) * row_bytes},
+                {rows, per_seq * width}, {row_len, per_seq}, {draft, nodes * row_bytes}, {mask, nodes * 8}, {n_tree, per_seq}};
+    constexpr int kOutputs = 3, kAll = 10;
+    for (int i = 0; i < kOutputs; i++)
+        for (int j = i + 1; j < kAll; j++)
+            if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes)) return GLM_ERR_INVALID_ARG;
     const size_t partials = glm::tree_partials(batch, n_nodes, H, width, sms);
     char *ws = static_cast<char *>(workspace);
     float *part_acc = reinterpret_cast<float *>(ws);
@@ -757,7 +767,13 @@ int glm_tree_commit(const glm_dsa_dims *dims, const void *draft, int32_t cache_f
         return GLM_ERR_INVALID_ARG;
     const int row_bytes = cache_format == GLM_CACHE_FP4 ? glm::kFp4RowBytes : glm::kRowBytes;
     const size_t drafts = static_cast<size_t>(batch) * n_nodes;
-    if (overlap(draft, drafts * row_bytes, cache, static_cast<size_t>(n_rows) * row_bytes)) return GLM_ERR_INVALID_ARG;
+    const size_t cache_bytes = static_cast<size_t>(n_rows) * row_bytes, from = drafts * glm::kIdxDim * 2;
+    const size_t to = static_cast<size_t>(batch) * ld_tokens * glm::kIdxDim * 2;
+    // (warps read their rows while others write theirs)
+    if (overlap(draft, drafts * row_bytes, cache, cache_bytes) || overlap(draft_k, from, k, to) ||
+        overlap(draft_k, from, gate, to) || overlap(draft_gate, from, k, to) || overlap(draft_gate, from, gate, to) ||
+        overlap(k, to, gate, to) || overlap(cache, cache_bytes, k, to) || overlap(cache, cache_bytes, gate, to))
+        return GLM_ERR_INVALID_ARG;
     const glm::TreeCommitArgs a{static_cast<const uint8_t *>(draft), row_bytes, path, batch, n_nodes, ld_path, slots,
                                 q_seq, q_pos, cu_new, n_cap, static_cast<uint8_t *>(cache), n_rows,
                                 static_cast<const uint16_t *>(draft_k), static_cast<const uint16_t *>(draft_gate),
