@@ -617,6 +617,19 @@ def _need(t, name, ndim):
     return t.shape, t.get_device()
 
 
+def _misfit(*tensors):
+    """The ValueError of the first of (tensor, name, dims or None) that is no tensor, or not of its dims."""
+    for t, name, ndim in tensors:
+        if not isinstance(t, torch.Tensor):
+            return ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != ndim if ndim is not None else t.dim() == 0:
+            return ValueError(f"{name} must have {ndim or 'more'} dims, got {t.dim()}")
+    return ValueError("bad shapes")
+
+
+_NO_SIZES = (AttributeError, IndexError, TypeError, ValueError)   # of a look at the sizes of what is no tensor, or has no such dims
+
+
 _I8, _U8, _T32, _T64, _BF = torch.int8, torch.uint8, torch.int32, torch.int64, torch.bfloat16
 
 
@@ -628,9 +641,12 @@ def _tree_mla(fn, name, dims, q, cache, rows, draft, mask, sm_scale, out, worksp
               row_bytes):
     shape, dev = _need(q, "q", 4)
     B, T, H, _ = shape
-    if rows.dim() != 2:
-        raise ValueError(f"rows must have 2 dims, got {rows.dim()}")
-    width, ws_bytes, per_seq = rows.shape[1], workspace.numel(), (B,)
+    try:
+        (_, width), per_seq, ws_bytes, cache_row, draft_row = rows.shape, (B,), workspace.numel(), cache.shape[-1], draft.shape[-1]
+    except _NO_SIZES:
+        raise _misfit((rows, "rows", 2), (workspace, "workspace", None), (cache, "cache", None), (draft, "draft", None)) from None
+    if cache_row != row_bytes or draft_row != row_bytes:
+        raise ValueError(f"cache and draft must be rows of {row_bytes} bytes, got {cache_row} and {draft_row}")
     p = _take(dev, (q, cache, rows, row_len, draft, mask, n_tree, out, lse, workspace), _TREE_TYPES[kind],
               ((B, T, dims.n_heads, 512), None, (B, width), per_seq, None, (B, T), per_seq, shape, (B, T, dims.n_heads), None),
               _TREE_NAMES)
@@ -687,8 +703,10 @@ def glm_block_tables(length, n_new, n_blocks, block_table, free, n_free, block_s
     per_seq, dev = _need(length, "length", 1)
     _need(block_table, "block_table", 2)
     B, ld_blocks = block_table.shape
-    ld_slot = 0 if slot_map is None else slot_map.shape[-1]
-    packed, pool, one = slots.shape, free.shape, (1,)
+    try:
+        packed, pool, one, ld_slot = slots.shape, free.shape, (1,), 0 if slot_map is None else slot_map.shape[1]
+    except _NO_SIZES:
+        raise _misfit((slots, "slots", None), (free, "free", None), (slot_map, "slot_map", 2)) from None
     p = _take(dev, (length, n_new, n_blocks, pad, block_table, free, n_free, slots, q_seq, q_pos, slot_map, len_out, n_blocks_out,
                     cu_new, free_out, n_free_out), _TABLES_TYPES,
               (None, per_seq, per_seq, per_seq, (B, ld_blocks), None, one, None, packed, packed, (B, ld_slot), per_seq, per_seq,
@@ -712,11 +730,14 @@ def glm_tree_commit(dims, draft, path, n_nodes, slots, q_seq, q_pos, cu_new, cac
     cu_new of glm_block_tables; draft_k, draft_gate bf16 [B, n_nodes, 128] with k, gate bf16
     [B, ld_tokens, 128], or none of the four."""
     (B, ld_path), dev = _need(path, "path", 2)
-    kind, row, packed = draft.dtype, draft.shape[-1], slots.shape
+    try:
+        kind, row, cache_row, packed = draft.dtype, draft.shape[-1], cache.shape[-1], slots.shape
+        ld_tokens = 0 if k is None else k.shape[1]
+    except _NO_SIZES:
+        raise _misfit((draft, "draft", None), (cache, "cache", None), (slots, "slots", None), (k, "k", 3)) from None
     fmt = _COMMIT_FORMAT.get((kind, row))
-    if fmt is None or cache.shape[-1] != row:
-        raise ValueError(f"draft and cache must be rows of one format, got {kind} rows of {row} and {cache.shape[-1]}")
-    ld_tokens = 0 if k is None else k.shape[1]
+    if fmt is None or cache_row != row:
+        raise ValueError(f"draft and cache must be rows of one format, got {kind} rows of {row} and {cache_row}")
     drafts, state = (B, n_nodes, 128), (B, ld_tokens, 128)
     p = _take(dev, (draft, path, slots, q_seq, q_pos, cu_new, cache, draft_k, draft_gate, k, gate), _COMMIT_TYPES[kind],
               ((B * n_nodes, row), None, None, packed, packed, (B + 1,), None, drafts, drafts, state, state), _COMMIT_NAMES)
