@@ -16,11 +16,13 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libglm_dsa.so")
 
-for _built in (LIB_PATH, os.path.join(_HERE, "_args.so")):
-    if not os.path.exists(_built):
-        raise ImportError(f"{_built} is missing: build it with `python kpool_indexer_int8_b200/build.py`")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python kpool_indexer_int8_b200/build.py`")
 
-from . import _args                                        # noqa: E402  (the built checks of csrc/args.c)
+try:
+    from . import _args                                    # the built checks of csrc/args.c
+except ImportError:                                        # (not built, or for another Python: the checks below do)
+    _args = None
 
 lib = C.CDLL(LIB_PATH)
 
@@ -562,8 +564,12 @@ lib.glm_tree_commit.argtypes = [_D, _P, _I32, _P, _I32, _I32, _I64, _P, _P, _P, 
 lib.glm_tree_commit.restype = C.c_int
 
 
-_args.setup(torch.Tensor, [(torch.int8, 0, 8), (torch.int32, 0, 32), (torch.int64, 0, 64), (torch.uint8, 1, 8),
-                           (torch.float32, 2, 32), (torch.bfloat16, 4, 16)])   # DLPack: 0 int, 1 uint, 2 float, 4 bfloat
+if _args is not None:
+    try:
+        _args.setup(torch.Tensor, [(torch.int8, 0, 8), (torch.int32, 0, 32), (torch.int64, 0, 64), (torch.uint8, 1, 8),
+                                   (torch.float32, 2, 32), (torch.bfloat16, 4, 16)])   # DLPack: 0 int, 1 uint, 2 float, 4 bfloat
+    except (AttributeError, ImportError, ValueError):      # a torch without the exchange table, or of another DLPack
+        _args = None
 _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -583,8 +589,9 @@ def _bad(t, dtype, shape, name, device):
 def _take(device, tensors, dtypes, shapes, names):
     """Addresses of the tensors (or None) of a call, checked against their types and shapes (None: any), all
     contiguous on one device. The checks of a decode step's calls are on its critical path, so they are
-    native; a tensor that fails them (or that the native code cannot see) is looked at again here."""
-    return _args.take(device, tensors, dtypes, shapes) or \
+    native where they are built; a tensor that fails them (or that the native code cannot see) is looked at
+    again here."""
+    return _args is not None and _args.take(device, tensors, dtypes, shapes) or \
         [_address(device, *n) for n in zip(tensors, dtypes, shapes, names)]
 
 

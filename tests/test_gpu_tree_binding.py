@@ -75,3 +75,13 @@ def test_tensors_of_another_rank_are_a_value_error(cuda):
     for name in ("draft", "path", "cache", "k"):
         with pytest.raises(ValueError, match=name):
             kp.glm_tree_commit(dims, **dict(commit, **{name: commit[name].reshape(-1)}))
+
+
+def test_the_checks_in_python_are_the_native_ones(cuda, monkeypatch):
+    # without csrc/args.c: the same calls are taken and refused
+    from tests import test_gpu_block_tables, test_gpu_tree_edges
+    monkeypatch.setattr(kp, "_args", None)
+    test_gpu_tree_edges.test_binding_refuses(cuda)
+    test_gpu_tree_edges.test_views_and_an_empty_cache(cuda, 4)
+    test_gpu_block_tables.run(cuda, test_gpu_block_tables.request_batch(np.random.default_rng(1), 5, 16, 90, 20, pads=True), 120, 130)
+    test_gpu_block_tables.run_commit(cuda, commit_case(np.random.default_rng(2), 3, 5, "fp4", 5, 4))
