@@ -77,10 +77,13 @@ struct PrLayout {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// One arrival on a barrier of the pair's first CTA. What it announces stays in the arriving CTA (operands
-// in its shared memory, behind a proxy fence, and tensor memory, behind a tcgen05 fence), so the
-// arrival needs no ordering across the cluster: with release at cluster scope each of the four
-// arrivals of a tile waited 900 to 1,400 cycles for the warp's outstanding memory traffic.
+// One arrival on a barrier of the pair's first CTA, whose tensor-core warp then issues products for both. It announces
+// operands in the arriving CTA's own shared memory, made visible to that CTA's tensor core by the proxy fence before
+// it, and tensor memory, behind a tcgen05 fence: neither goes through the other CTA, and the arrival follows both in the
+// arriving warp. The memory model's own form of this is an arrival with release, and a wait with acquire, at cluster
+// scope. Such an arrival waits 900 to 1,400 cycles for the warp's copies in flight, in each of the four a tile;
+// passed on by the second CTA's idle tensor-core warp, 8 nodes over 262,144 rows take 399 us a call for 385, a batch
+// of selected FP8 lists 75 for 66.6 (of which the hop itself 5).
 __device__ __forceinline__ void arrive_leader(uint32_t mbar) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\t"
