@@ -31,6 +31,8 @@
 // would allow 2,000. 262,144 4-bit rows, 16 query rows: 74 us a call with the merge, 1.1 TB/s; the rows at
 // the copy rate would take 12. A small call is bound by its start and end and, cold, by its
 // instructions: 67 int8 keys and 64 query rows take 9.8 us of the GPU.
+#include <algorithm>
+
 #include "tree_mla_common.cuh"
 
 namespace glm {
@@ -590,6 +592,16 @@ cudaError_t launch_tree_t(const TreePlan &p, const TreeArgs &a, float *part_acc,
 constexpr int kTrMaxParts = 1024;              // partials of one query that the combine kernel merges
 constexpr int kTrLevels = 4;                   // waves of runs to balance lists of different lengths
 
+// Waves of runs that a batch of long lists may be cut into: so many that its (sequence, tile of query rows) pairs have three
+// runs each or more, where one wave has two or three for some of them and none to balance with (8 sequences of 16
+// nodes of 64 heads, 64 tiles of query rows for 74 pairs of SMs, lists of 4,000 to 32,768 rows: 654 us with one wave, 469
+// with two, 487 with three, 514 with four; of 32,768 to 262,144: 5,050, 3,016, 2,912, 2,890). Where one wave
+// has enough, more only write and merge more partials (8 sequences of 4 nodes, up to 60,000 rows: 220 us with one,
+// 242, 268 and 305; 16 single tokens of 16 heads, 1,000 to 65,536 4-bit rows: 153, 183, 213, 247).
+int tree_levels(long long base, int units) {
+    const long long n = (3 * base + units - 1) / std::max(units, 1);
+    return static_cast<int>(std::min(std::max(n, 1ll), static_cast<long long>(kTrLevels)));
+}
 long long tree_tiles(long long width, int keys) { return (width + keys - 1) / keys + 1; }
 
 }  // namespace
@@ -605,11 +617,14 @@ TreePlan tree_plan(int batch, int n_nodes, int n_heads, int width, int num_sms) 
     p.q_tiles = (rows + p.nq - 1) / p.nq;
     p.units = pair ? num_sms / 2 : num_sms;
     const long long tiles = tree_tiles(width, pair ? kTreePairKeys : kTrKeys), base = static_cast<long long>(batch) * p.q_tiles;
-    // one wave of runs when the lists are short (or there is one); else the kernel weighs up to four
-    // against the lists' lengths
-    p.levels = batch > 1 && base * tiles > 32ll * p.units ? kTrLevels : 1;
+    // One wave of runs when the lists are short, up to 32 tiles an SM, or there is one (4 sequences of 13 nodes, up to 4,096
+    // rows, 17 tiles a pair: 48.3 us a call, 75.5 with two waves); else the kernel weighs up to so many
+    // against the lists' lengths.
+    p.levels = batch > 1 && base * tiles > 32ll * p.units ? tree_levels(base, p.units) : 1;
     long long parts = base >= static_cast<long long>(p.levels) * p.units ? 1 : p.levels * static_cast<long long>(p.units) / base;
-    if (batch > 1 && parts > 1) parts *= 2;    // a list twice as long as the mean
+    // twice as many, for a list longer than the mean (those sequences: 48.3 us a call, 73 without, 70 with four times;
+    // 16 of up to 100,000 rows, 64 query rows: 359, 588 and 376)
+    if (batch > 1 && parts > 1) parts *= 2;
     if (parts > tiles) parts = tiles;
     if (parts > kTrMaxParts) parts = kTrMaxParts;
     // A few tiles (of this bound, one more than the list has) are one run, without a merge: 64 query rows over
@@ -625,8 +640,9 @@ size_t tree_partials(int batch, int n_nodes, int n_heads, int width, int num_sms
     const long long rows = static_cast<long long>(n_nodes) * n_heads, all = tree_tiles(width, kTrKeys);
     const long long tiles = all > kTrMaxParts ? kTrMaxParts : all;
     const int nq = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    const long long base = batch * ((rows + 127) / 128);
     int waves = batch > 1 ? 2 : 1;
-    if (batch > 1 && batch * ((rows + 127) / 128) * all > 32ll * (num_sms / 2)) waves *= kTrLevels;
+    if (batch > 1 && base * all > 32ll * (num_sms / 2)) waves *= tree_levels(base, num_sms / 2);
     const long long cap = static_cast<long long>(waves) * num_sms * nq;
     return static_cast<size_t>(batch * rows * tiles < cap ? batch * rows * tiles : cap);
 }
