@@ -473,7 +473,8 @@ int glm_tree_mla_decode_fp4(const glm_dsa_dims *dims, const void *q_dev, const u
  *   len_out, n_blocks_out  int32 [batch] (0 of ended requests);  cu_new int32 [batch + 1]: packed offsets
  *         (every n_new > 0 counts, refused or not; saturates at INT32_MAX)
  *   free_out, n_free_out   int32 [free_cap], [1]: what is left of the stack, then the blocks of ended
- *         requests in request order (entries past n_free_out are not written)
+ *         requests in request order (entries past n_free_out are not written; blocks past free_cap are dropped:
+ *         free_cap >= pool_blocks holds them all)
  * The outputs (other than block_table and slot_map) must not be the inputs: CTAs read what others
  * write. Calling again with the same inputs gives the same outputs. 0 <= batch <= 8192,
  * 1 <= block_size <= 65536, pool_blocks * block_size <= INT32_MAX (cache rows are int32 in index lists).

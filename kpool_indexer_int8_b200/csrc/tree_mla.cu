@@ -28,9 +28,9 @@
 // What bounds it: with 16 query rows and a long list, the chain from a free C tile through widening
 // (about 700 cycles), S (32 products of 23, 1,100 with their latency), softmax (1,700) and O (900), of which
 // two are in flight: a 64-key tile takes 3,300 cycles, where shared memory (C written once and read twice)
-// would allow 2,000. 262,144 4-bit rows, 16 query rows: 74 us a call with the merge, 1.1 TB/s; the rows at
-// the copy rate would take 12. A small call is bound by its start and end and, cold, by its
-// instructions: 67 int8 keys and 64 query rows take 9.8 us of the GPU.
+// would allow 2,000. 262,144 4-bit rows, 16 query rows: 73 us a call with the merge, 1.1 TB/s; the rows at
+// the copy rate would take 12. A small call is bound by the latencies of its start, two tiles and end (35 % of
+// the warps' time waits for loads, 6 % for instructions): 67 int8 keys and 64 query rows take 9.7 us of the GPU.
 #include <algorithm>
 
 #include "tree_mla_common.cuh"

@@ -9,21 +9,22 @@
 // often. Roles of the 15 warps of a CTA, each with its own raw rows in shared memory, filled by
 // asynchronous copies a tile ahead:
 //   * warps 0-3 (softmax): one thread per row and half of the keys (tensor-memory lane = row, the
-//     upper 64 lanes hold the tile's upper 48 keys): references, sums and P' as in tree_mla.cu, the
-//     two halves of a row meeting only when a reference moves;
+//     upper 64 lanes hold the tile's upper 48 keys): references, sigmas, sums and P' as in tree_mla.cu, the
+//     two halves of a row meeting only when one of them may have to move;
 //   * warps 4-9 (K): whole rows of the CTA's 48 keys as fp16 once S(t - 1) is done, and the scales of all 96;
 //   * warps 10-13 (V): the CTA's 256 dims of the 96 keys once O of t - 1 is done;
 //   * warp 14 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs.
 // K, V and P have one buffer each: shared memory holds no more beside Q.
 //
-// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,645 cycles of a CTA: 2,150 cycles of
-// shared-memory wavefronts of the warps (counted; rows copied in and read, 49 KB each way, K and V 48 KB each
-// and P 12 KB written, scales, barriers) and 172 KB of operands read by the tensor cores (Q 64, K 48, V
-// 48, P 12), 1,380 cycles: 97 %. Tensor pipe 42 % active, issue 46 %. 8 nodes of 64 heads over 262,144
-// int8 rows: 369 us a call, 745 TFLOP/s (350 us and 785 alone on a cool chip), 0.45 of the measured
-// bf16 rate; 372 with P read for each of its two products. What was tried on top of it and did not pay:
+// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,725 cycles of a CTA. The tensor cores read 172 KB of
+// operands (Q 64, K 48, V 48, P 12), 1,380 cycles; the warps' own bytes (rows copied in and read, 49 KB each way, K
+// and V 48 KB each and P 12 KB written) are 1,650, with scales, barriers and partials 1,870 wavefronts, and 310 more are
+// counted as bank conflicts, whose cause is not known (the addresses here have none). Tensor pipe 41 % active,
+// issue 46 %. 8 nodes of 64 heads over 262,144 int8 rows: 385 us a call back to back, under the power limit, 350 and
+// 785 TFLOP/s one at a time, 0.48 of the measured bf16 rate. What was tried on top of it and did not pay (against 369 then):
 // two teams of softmax warps on alternate tiles (410 us), eight softmax warps on one tile (386), rows read
-// in rolled loops right before they are widened (390-404), one set of warps for K and V (391).
+// in rolled loops right before they are widened (390-404), one set of warps for K and V (391), P read for each of its
+// two products (372), P' tested for fp16's range after the exponentials with the scores read again to move (389).
 #include "tree_mla_common.cuh"
 
 namespace glm {
