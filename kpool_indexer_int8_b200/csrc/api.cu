@@ -672,7 +672,8 @@ int tree_mla_entry(const glm_dsa_dims *dims, const void *q, const void *cache, i
     a.give_up = g_tree_waits_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const glm::TreePlan plan = glm::tree_plan(batch, n_nodes, H, width, sms);
-    if (plan.parts > 1 && static_cast<size_t>(batch) * n_nodes * H * plan.parts > partials) return GLM_ERR_WORKSPACE;
+    // (holds for every shape, see tree_partials; a launch is never to depend on it)
+    if (plan.parts > 1 && nodes * H * plan.parts > partials) return GLM_ERR_WORKSPACE;
     rc = cuda_status(glm::launch_tree_mla(plan, a, format, part_acc, part_ml, st));
     if (rc != GLM_OK || plan.parts == 1) return rc;
     return cuda_status(

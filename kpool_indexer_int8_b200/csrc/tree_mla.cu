@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             const bool key = lane < 16 && val[buf * kTrKeys + j] != 0;
             const float sc = key ? scl[buf * kTrKeys + j] : 0.0f;
             // What a row's score may be beyond kTop: its p, and p scale / sigma, at most 2^kTop (a row without a reference:
-            // none). And scale / sigma: a scale far above sigma, or a NaN, has a weight of 0, or the score is NaN; the product
-            // of the weight with it must be 0 too. With 16 query rows while S is being made; with 32 the registers for it spill (92.5 us for 89.3 over
-            // 262,144 int8 rows).
+            // none). And scale / sigma: a scale far above sigma, or a NaN, has a weight of 0, or the score is NaN; the
+            // product of the weight with it must be 0 too. With 16 query rows while S is being made; with 32 the
+            // registers for it spill (92.5 us for 89.3 over 262,144 int8 rows).
             float most[V], over[V];
             const float lg = sc > 0.0f ? __log2f(sc) : -150.0f;
             auto load_most = [&]() {
