@@ -27,8 +27,8 @@
 //
 // What bounds it: with 16 query rows and a long list, the chain from a free C tile through widening
 // (about 700 cycles), S (32 products of 23, 1,100 with their latency), softmax (1,700) and O (900), of which
-// two are in flight: a 64-key tile takes 3,300 cycles, where shared memory (C written once and read twice)
-// would allow 2,000. 262,144 4-bit rows, 16 query rows: 73 us a call with the merge, 1.1 TB/s; the rows at
+// two are in flight: a 64-key tile takes 3,200 cycles, where shared memory (C written once and read twice)
+// would allow 2,000. 262,144 4-bit rows, 16 query rows: 72 us a call with the merge, 1.1 TB/s; the rows at
 // the copy rate would take 12. A small call is bound by the latencies of its start, two tiles and end (35 % of
 // the warps' time waits for loads, 6 % for instructions): 67 int8 keys and 64 query rows take 9.7 us of the GPU.
 #include <algorithm>
@@ -44,7 +44,7 @@ using namespace tree;
 constexpr int kTrSoft = 8;                     // warps 0-7 softmax, then the widening warps and one for the tensor cores
 constexpr int kTrKeys = 64;                    // keys of a tile
 
-enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbSFree = 6, kTbP = 8, kTbEnd = 10, kTbCount };
+enum TrBar { kTbFull = 0, kTbDone = 2, kTbS = 4, kTbP = 6, kTbEnd = 8, kTbCount };
 
 template <int NQ>
 struct TrLayout {
@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tc::mbar_init(bar(kTbFull + i), L::kWiden);
                 tc::mbar_init(bar(kTbDone + i), 1);
                 tc::mbar_init(bar(kTbS + i), 1);
-                tc::mbar_init(bar(kTbSFree + i), 8);
                 tc::mbar_init(bar(kTbP + i), 8);
             }
             tc::mbar_init(bar(kTbEnd), 1);
@@ -336,9 +335,9 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             }
             if (early) accumulate(i - 1);
             wait(kTbFull + buf, i >> 1);
-            if (i >= 2) wait(kTbSFree + buf, (i >> 1) - 1);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
+            // (S(i - 2), which this one is written over, has been read: O of it was issued above, after P(i - 2))
             if (tc::elect_one()) {   // S^T = C(i) . Q^T: M = 64 keys, K = 512
                 const uint64_t ca = dc + ((buf * L::kCBytes) >> 4);
 #pragma unroll
@@ -411,8 +410,6 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 tr_tmem_ld<V>(tmem + lanes + kSCol + buf * NQ + c0, r);
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(kTbSFree + buf));
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
                     const float4 f = f4[e >> 1];

@@ -16,11 +16,11 @@
 //   * warp 14 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs.
 // K, V and P have one buffer each: shared memory holds no more beside Q.
 //
-// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,725 cycles of a CTA. The tensor cores read 172 KB of
+// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,690 cycles of a CTA. The tensor cores read 172 KB of
 // operands (Q 64, K 48, V 48, P 12), 1,380 cycles; the warps' own bytes (rows copied in and read, 49 KB each way, K
 // and V 48 KB each and P 12 KB written) are 1,650, with scales, barriers and partials 1,870 wavefronts, and 310 more are
-// counted as bank conflicts, whose cause is not known (the addresses here have none). Tensor pipe 41 % active,
-// issue 46 %. 8 nodes of 64 heads over 262,144 int8 rows: 385 us a call back to back, under the power limit, 350 and
+// counted as bank conflicts, whose cause is not known (the addresses here have none). Tensor pipe 42 % active,
+// issue 47 %. 8 nodes of 64 heads over 262,144 int8 rows: 386 us a call back to back, under the power limit, 350 and
 // 785 TFLOP/s one at a time, 0.48 of the measured bf16 rate. What was tried on top of it and did not pay (against 369 then):
 // two teams of softmax warps on alternate tiles (410 us), eight softmax warps on one tile (386), rows read
 // in rolled loops right before they are widened (390-404), one set of warps for K and V (391), P read for each of its
@@ -45,7 +45,7 @@ constexpr int kPrMeta = 3;                     // tiles whose scales are kept
 constexpr uint32_t kPrSCol = 256;              // two score accumulators of 48 columns after the output's 256
 constexpr uint32_t kPrSStep = 64;
 
-enum PrBar { kPbK = 0, kPbV, kPbP, kPbSFree, kPbS = 5, kPbDone = 7, kPbMeta = 9, kPbEnd = 12, kPbCount };
+enum PrBar { kPbK = 0, kPbV, kPbP, kPbS, kPbDone = 5, kPbMeta = 7, kPbEnd = 10, kPbCount };
 
 struct PrLayout {
     static constexpr int kQ = 0;                                 // 8 row groups x 64 dim groups x 128 B
@@ -82,7 +82,7 @@ __device__ __forceinline__ void cluster_sync() {
 // operands in the arriving CTA's own shared memory, made visible to that CTA's tensor core by the proxy fence before
 // it, and tensor memory, behind a tcgen05 fence: neither goes through the other CTA, and the arrival follows both in the
 // arriving warp. The memory model's own form of this is an arrival with release, and a wait with acquire, at cluster
-// scope. Such an arrival waits 900 to 1,400 cycles for the warp's copies in flight, in each of the four a tile;
+// scope. Such an arrival waits 900 to 1,400 cycles for the warp's copies in flight, in each of the three a tile;
 // passed on by the second CTA's idle tensor-core warp, 8 nodes over 262,144 rows take 399 us a call for 385, a batch
 // of selected FP8 lists 75 for 66.6 (of which the hop itself 5).
 __device__ __forceinline__ void arrive_leader(uint32_t mbar) {
@@ -226,7 +226,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             tc::mbar_init(bar(kPbV), 2 * kPrV);
             tc::mbar_init(bar(kPbP), 2 * kPrSoft);
             for (int i = 0; i < 2; i++) {
-                tc::mbar_init(bar(kPbSFree + i), 2 * kPrSoft);
                 tc::mbar_init(bar(kPbS + i), 1);
                 tc::mbar_init(bar(kPbDone + i), 1);
             }
@@ -403,8 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 __syncwarp();
             };
             for (int i = 0; i < n_tiles; i++) {
-                wait(kPbK, i);
-                if (i >= 2) wait(kPbSFree + (i & 1), (i >> 1) - 1);
+                wait(kPbK, i);   // (S(i - 2), which this one is written over, has been read: O of it is issued, after P(i - 2))
                 ok = __all_sync(0xffffffffu, ok);
                 tc::fence_after_sync();
                 if (tc::elect_one()) {   // S(i) = Q K(i)^T: N = 96 keys, K = 512
@@ -457,8 +455,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 tc::tmem_ld16(tmem + lanes + kPrSCol + (i & 1) * kPrSStep + 32, s1);
                 tc::tmem_wait_ld();
                 tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) arrive_leader(bar(kPbSFree + (i & 1)));
                 const uint64_t qk2 = pack2(qk, qk), ref2 = pack2(-scaling.ref, -scaling.ref);
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e += 4) {
