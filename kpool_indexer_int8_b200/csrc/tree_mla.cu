@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             // product of the weight with it must be 0 too. With 16 query rows while S is being made; with 32 the
             // registers for it spill (92.5 us for 89.3 over 262,144 int8 rows).
             float most[V], over[V];
-            const float lg = sc > 0.0f ? __log2f(sc) : -150.0f;
+            const float mag = fabsf(sc), lg = mag > 0.0f ? __log2f(mag) : -150.0f;
+            const uint32_t sign = sc < 0.0f ? 0x80008000u : 0u;   // (unwritten drafts, that nobody sees, may have any)
             auto load_most = [&]() {
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
@@ -389,10 +390,10 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 for (int e = 0; e < V; e += 4) {
                     if (e < e0 || e >= e0 + n) continue;
                     const float4 f = inv4[e >> 2];
-                    over[e] = fminf(sc * f.x, kFltMax);
-                    over[e + 1] = fminf(sc * f.y, kFltMax);
-                    over[e + 2] = fminf(sc * f.z, kFltMax);
-                    over[e + 3] = fminf(sc * f.w, kFltMax);
+                    over[e] = fminf(mag * f.x, kFltMax);
+                    over[e + 1] = fminf(mag * f.y, kFltMax);
+                    over[e + 2] = fminf(mag * f.z, kFltMax);
+                    over[e + 3] = fminf(mag * f.w, kFltMax);
                 }
             };
             constexpr bool kEarly = V <= 8;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 float m[V];
 #pragma unroll
                 for (int e = 0; e < V; e++) m[e] = x[e];
-                const float bx = butterfly<V, true>(m), ls = sc > 0.0f ? lg : -INFINITY;
+                const float bx = butterfly<V, true>(m), ls = mag > 0.0f ? lg : -INFINITY;
 #pragma unroll
                 for (int e = 0; e < V; e++) m[e] = x[e] + ls;
                 const float by = butterfly<V, true>(m);
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                     const float p0 = exp2_approx(x[8 * g + e]), p1 = exp2_approx(x[8 * g + e + 1]);
                     l[8 * g + e] += p0;
                     l[8 * g + e + 1] += p1;
-                    p4[e >> 1] = f16x2_rn(p0 * over[8 * g + e], p1 * over[8 * g + e + 1]);
+                    p4[e >> 1] = f16x2_rn(p0 * over[8 * g + e], p1 * over[8 * g + e + 1]) ^ sign;
                 }
                 if (lane < 16) *reinterpret_cast<uint4 *>(line + g * 128) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
             }

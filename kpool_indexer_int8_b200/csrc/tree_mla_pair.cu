@@ -307,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 for (int h = 0; h < 2; h++)
                     v[r][h] = R::line(codes + r * R::kCodes, tails + r * R::kTail, lane + 32 * h, lane / 2 + 16 * h);
             const unsigned bits = __ballot_sync(0xffffffffu, rows != -1);
-            const float mx = finite_max(holds ? sc : 0.0f), lg = __log2f(sc);
+            const float mx = finite_max(holds ? fabsf(sc) : 0.0f), lg = __log2f(fabsf(sc));
             // the next rows, into the slots just read
             const int nxt = row_of(t + 1, my_key, e1);
             if (i + 1 < n_tiles) R::template fetch<kN>(codes, tails, a, nxt, 0, has_drafts(t + 1));
@@ -528,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
                 partial = true;
 #pragma unroll 1
                 for (int e = 0; e < kPrHalf; e++)
-                    if (!(scl[m * kPrKeys + key0 + e] * inv <= kFltMax)) keys &= ~(1ull << e);
+                    if (!(fabsf(scl[m * kPrKeys + key0 + e]) * inv <= kFltMax)) keys &= ~(1ull << e);
             }
             uint32_t p[kPrHalf / 2];
             const uint64_t inv2 = pack2(inv, inv);

@@ -121,3 +121,41 @@ def test_a_long_tail_far_below_the_peaks(cuda, fmt, H):
     err = np.abs(out[0, 0].float().cpu().numpy().astype(np.float64) - want)
     assert (err <= tol).all(), float((err / tol).max())
     assert (np.abs(lse[0, 0].cpu().numpy() - wl) <= ltol).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("value", [-2.0 ** 16, -1e30, -FLT_MAX, -np.inf, "bytes"])
+def test_drafts_that_nobody_has_written(cuda, fmt, cut, value):
+    # rows of a tree's unused places as they may lie in memory: scales of either sign, or any bytes
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 4)
+    c = case(rng, fmt, b, T, H, width, [width - i % 60 for i in range(b)], [T] * b, n_rows=700)
+    rows = [s * T + j for s in range(b) for j in (1, 4, 5)]
+    if value == "bytes":
+        c["draft"].view(np.uint8)[rows] = rng.integers(0, 256, (len(rows), c["draft"].shape[1]), dtype=np.uint8)
+    else:
+        set_scale(c["draft"], rows, fmt, value)
+    c["masks"] = [[0b000001, 0, 0b000101, 0b001001, 0b001000, 0]] * b
+    check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("ratio", [1.0, 2.0 ** 20])
+def test_rows_with_negative_scales(cuda, fmt, cut, ratio):
+    # code times scale is what a row holds, whatever its sign; one of them far above the others and, seen, of no weight
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 5)
+    c = case(rng, fmt, b, T, H, width, [width] * b, [T] * b, n_rows=700)
+    sc = R.row_scales(c["cache"], np.arange(700), fmt)
+    sc[rng.random(700) < 0.5] *= -1.0
+    set_scale(c["cache"], np.arange(700), fmt, sc.astype(np.float32))
+    c["q"] = synth.f32_to_bf16_bits(synth.bf16_bits_to_f32(c["q"]) + np.float32(0.5))
+    c["cache"].view(np.uint8)[7, :288 if fmt == "fp4" else 512] = {"int8": 100, "fp8": 0x7E, "fp4": 0x22}[fmt]
+    if fmt == "fp4":
+        c["cache"].view(np.uint8)[7, 256:288] = 0x7E
+    set_scale(c["cache"], [7], fmt, -float(np.median(np.abs(sc))) * 1024 * ratio)
+    c["rows"][c["rows"] == 7] = 8
+    c["rows"][:, width // 3] = 7
+    check(c, *launch(c, cuda))

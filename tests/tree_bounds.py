@@ -42,6 +42,7 @@ def node(q, c, scales, sm_scale, times=None):
     drift = dp.sum(1)
     sums = (times.sum() / 8 + 80) * U32
     spread = p @ mag
+    scales = np.abs(scales)
     codes = np.where(scales[:, None] > 0, mag / np.where(scales > 0, scales, 1.0)[:, None], 0.0)
     w = one * scales[None]
     flush = (times * np.minimum(w, FLUSH * w.max(1, keepdims=True))) @ codes
