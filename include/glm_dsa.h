@@ -428,8 +428,8 @@ int glm_mla_v_up(const glm_dsa_dims *dims, const void *o_lat_dev, const void *w_
  * whose own row is not in the cache yet. A row that a node does not see has no effect on it, whatever it holds; a NaN
  * or an infinite scale that it sees makes it NaN. The products run on the tensor cores with fp16 operands and fp32
  * accumulation: codes and (scaled by powers of two) queries exactly, a softmax weight times its row's scale as one
- * fp16 number (off by 2^-11 of itself, or 2^-32 of the largest that the query row sees; glm_sparse_mla_decode
- * carries 22 bits), sums and references in fp32.
+ * fp16 number (off by 2^-11 of itself, or 2^-32 of the largest that the query row sees), or, with up to 16 query
+ * rows (nodes times heads) and in small calls, two (2^-22, as in glm_sparse_mla_decode); sums and references in fp32.
  */
 int glm_tree_mla_decode(const glm_dsa_dims *dims, const void *q_dev, const int8_t *cache_dev, int64_t n_rows,
                         const int32_t *rows_dev, const int32_t *row_len_dev, int32_t width,

@@ -20,16 +20,18 @@
 //     vote of the eight warps per tile): then the accumulator in tensor memory is rescaled, otherwise no
 //     maximum is taken. Sums stay in registers, one per thread and query row, until the end.
 // P' is one fp16 term: a weight is off by at most 2^-11 of itself (an eighth of the bf16 output's 2^-8), or,
-// once P' is below 2^-14, by 2^-24 - kHead of the row's largest weight times scale. A second term, as the sparse attention
-// has it, would double the products with the values: by themselves 58 us of a pair's 379 over 262,144 rows.
+// once P' is below 2^-14, by 2^-24 - kHead of the row's largest weight times scale. Tiles of 16 query rows carry what it
+// leaves as a second term, as the sparse attention does (2^-22): 16 more columns of N, 73.7 us for 71.6 over
+// 262,144 4-bit rows. With 32 rows that takes 93 us for 87, with 64 shared memory has no room for it, and in a
+// pair, where it doubles the products with the values, those alone take 58 us more than its 379.
 //
 // A sequence's keys are cut into runs so that the CTAs fill the SMs; tree_combine.cu merges the
 // partials. Every wait is bounded; one that gives up sets the status word and the CTA writes NaN.
 //
 // What bounds it: with 16 query rows and a long list, the chain from a free C tile through widening
 // (about 700 cycles), S (32 products of 23, 1,100 with their latency), softmax (1,700) and O (900), of which
-// two are in flight: a 64-key tile takes 3,200 cycles, where shared memory (C written once and read twice)
-// would allow 2,000. 262,144 4-bit rows, 16 query rows: 72 us a call with the merge, 1.1 TB/s; the rows at
+// two are in flight: a 64-key tile takes 3,300 cycles, where shared memory (C written once and read twice)
+// would allow 2,000. 262,144 4-bit rows, 16 query rows: 74 us a call with the merge, 1.1 TB/s; the rows at
 // the copy rate would take 12. A small call is bound by the latencies of its start, two tiles and end (35 % of
 // the warps' time waits for loads, 6 % for instructions): 67 int8 keys and 64 query rows take 9.7 us of the GPU.
 #include <algorithm>
@@ -52,7 +54,9 @@ struct TrLayout {
     static constexpr int kCBytes = kTrKeys * 1024;
     static constexpr int kC = 0;                                 // [2] tiles: 8 blocks of 64 dims x 64 keys x 128 B, swizzled
     static constexpr int kQ = kC + 2 * kCBytes;                  // NQ/8 row groups x 64 dim groups x 128 B
-    static constexpr int kPBytes = kTrKeys * 2 * NQ;
+    static constexpr int kTerms = NQ == 16 ? 2 : 1;               // fp16 numbers of a weight: columns of P' beside each other
+    static constexpr int kNP = kTerms * NQ;
+    static constexpr int kPBytes = kTrKeys * 2 * kNP;
     static constexpr int kPBufs = NQ == 64 ? 1 : 2;              // (what else shared memory holds of 64 rows)
     static constexpr int kP = kQ + NQ * 1024;                    // [kPBufs] P', core matrices of 8 keys x 8 query rows
     static constexpr int kWiden = 8;                              // widening warps
@@ -92,9 +96,9 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     using R = Row<kFmt>;
     constexpr int kThreads = L::kThreads, kTrWarpMma = kTrSoft + L::kWiden;
     constexpr int V = NQ / 2;                                 // query rows of a softmax thread
-    constexpr int kLboP = 16 * NQ;                            // P': bytes between groups of 8 keys
-    constexpr uint32_t kSCol = 4 * NQ;                        // two score accumulators after the output's 4 tiles
-    constexpr int kCols = 6 * NQ <= 128 ? 128 : (6 * NQ <= 256 ? 256 : 512);
+    constexpr int NP = L::kNP, kLboP = 16 * NP;               // P': bytes between groups of 8 keys
+    constexpr uint32_t kSCol = 4 * NP;                        // two score accumulators after the output's 4 tiles
+    constexpr int kCols = 4 * NP + 2 * NQ <= 256 ? 256 : 512;   // (160, 192, 384)
     constexpr int kLow = (V == 32) ? 0 : (V == 16) ? 1 : 3;   // lane bits that repeat a query row in butterfly()
     constexpr int kShift = (V == 32) ? 0 : (V == 16) ? 1 : 2;
     pdl_begin(a.q, a.cache, a.rows, a.row_len, a.draft, a.mask, a.n_tree);
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
     } else if (warp == kTrWarpMma) {
         // ---------------- tensor cores ----------------
         constexpr uint32_t id_s = tc::idesc_f16(kTrKeys, NQ, false, false);
-        constexpr uint32_t id_o = tc::idesc_f16(128, NQ, true, true);
+        constexpr uint32_t id_o = tc::idesc_f16(128, NP, true, true);
         const uint64_t dq = tc::desc(tc::smem_addr(smem + L::kQ), 128, 8192);
         const uint64_t dc = tc::desc_sw128(tc::smem_addr(smem + L::kC), 1024);
         const uint64_t dct = tc::desc_sw128_mn(tc::smem_addr(smem + L::kC), 8192, 1024);
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
                 for (int ks = 0; ks < kTrKeys / 16; ks++)
 #pragma unroll
                     for (int mt = 0; mt < kLatent / 128; mt++)
-                        tc::mma_bf16(tmem + mt * NQ, ca + ((ks * 2048 + mt * 2 * 8192) >> 4), pa + ((ks * 2 * kLboP) >> 4),
+                        tc::mma_bf16(tmem + mt * NP, ca + ((ks * 2048 + mt * 2 * 8192) >> 4), pa + ((ks * 2 * kLboP) >> 4),
                                      id_o, (i > 0 || ks > 0) ? 1u : 0u);
                 tc::mma_commit(bar(kTbDone + buf));
             }
@@ -476,13 +480,13 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
 #pragma unroll 1
                     for (int mt = hh; mt < kLatent / 128; mt += 2) {
 #pragma unroll 1
-                        for (int cb = 0; cb < NQ; cb += CH) {
+                        for (int cb = 0; cb < NP; cb += CH) {
                             uint32_t o[CH];
-                            tr_tmem_ld<CH>(tmem + lanes + mt * NQ + cb, o);
+                            tr_tmem_ld<CH>(tmem + lanes + mt * NP + cb, o);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < CH; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[cb + e]);
-                            tc::tmem_st16(tmem + lanes + mt * NQ + cb, o);
+                            for (int e = 0; e < CH; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[cb % NQ + e]);
+                            tc::tmem_st16(tmem + lanes + mt * NP + cb, o);
                         }
                     }
                     tc::tmem_wait_st();
@@ -494,16 +498,23 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             unsigned char *line = smem + L::kP + (i % L::kPBufs) * L::kPBytes + (j >> 3) * kLboP + (c0 >> 3) * 128 + (j & 7) * 16;
 #pragma unroll
             for (int g = 0; g < V / 8; g++) {
-                uint32_t p4[4];
+                uint32_t p4[4], r4[4];                            // P' as fp16, and what that leaves of it
                 if constexpr (!kEarly) load_over(8 * g, 8);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     const float p0 = exp2_approx(x[8 * g + e]), p1 = exp2_approx(x[8 * g + e + 1]);
                     l[8 * g + e] += p0;
                     l[8 * g + e + 1] += p1;
-                    p4[e >> 1] = f16x2_rn(p0 * over[8 * g + e], p1 * over[8 * g + e + 1]) ^ sign;
+                    const float w0 = p0 * over[8 * g + e], w1 = p1 * over[8 * g + e + 1];
+                    const uint32_t h = f16x2_rn(w0, w1);
+                    p4[e >> 1] = h ^ sign;
+                    if constexpr (L::kTerms == 2) r4[e >> 1] = f16x2_rn(w0 - f16_lo_f(h), w1 - f16_hi_f(h)) ^ sign;
                 }
-                if (lane < 16) *reinterpret_cast<uint4 *>(line + g * 128) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
+                if (lane < 16) {
+                    *reinterpret_cast<uint4 *>(line + g * 128) = make_uint4(p4[0], p4[1], p4[2], p4[3]);
+                    if constexpr (L::kTerms == 2)
+                        *reinterpret_cast<uint4 *>(line + 16 * NQ + g * 128) = make_uint4(r4[0], r4[1], r4[2], r4[3]);
+                }
             }
             tc::fence_proxy_async();
             __syncwarp();
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
         // registers, 4 bytes a lane, 64 rows took 6,300 cycles
         constexpr int CH = 16;
         const int mt = warp >> 2, dim = mt * 128 + (warp & 3) * 32 + lane;
-        const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + mt * NQ;
+        const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + mt * NP;
 #pragma unroll 1
         for (int cb = 0; cb < NQ; cb += CH) {
             float f[CH];                                      // (read before the first write: the compiler keeps the order)
@@ -550,7 +561,15 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             for (int e = 0; e < CH; e += 4) *reinterpret_cast<float4 *>(f + e) = *reinterpret_cast<const float4 *>(alpha + cb + e);
             uint32_t o[CH];
             tr_tmem_ld<CH>(ta + cb, o);
-            tc::tmem_wait_ld();
+            if constexpr (L::kTerms == 2) {
+                uint32_t more[CH];
+                tr_tmem_ld<CH>(ta + NQ + cb, more);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < CH; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(more[e]));
+            } else {
+                tc::tmem_wait_ld();
+            }
 #pragma unroll
             for (int e = 0; e < CH; e++) {
                 float v = f[e] == -1.0f ? 0.0f : __uint_as_float(o[e]) * f[e];

@@ -19,11 +19,11 @@ FLT_MAX = float(np.finfo(np.float32).max)
 CUTS = [(2, 6, 4, 70), (8, 6, 4, 700), (4, 6, 10, 700), (150, 6, 10, 70), (2, 6, 40, 70), (2, 6, 40, 1500)]
 
 
-def check(c, out, lse, nodes=None, sm=SM):
+def check(c, out, lse, nodes=None, sm=SM, bits=11):
     """The nodes (None: all) of a call's first two and last sequences against the bounds."""
     o, l = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
     q = synth.bf16_bits_to_f32(c["q"]).astype(np.float64)
-    for b, i, want, wl, tol, ltol in B.tree(c, sm, q, sorted({0, 1, len(q) - 1} & set(range(len(q))))):
+    for b, i, want, wl, tol, ltol in B.tree(c, sm, q, sorted({0, 1, len(q) - 1} & set(range(len(q)))), bits):
         if nodes is not None and i not in nodes:
             continue
         if np.isneginf(wl).all():
@@ -159,3 +159,18 @@ def test_rows_with_negative_scales(cuda, fmt, cut, ratio):
     c["rows"][c["rows"] == 7] = 8
     c["rows"][:, width // 3] = 7
     check(c, *launch(c, cuda))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("b,T,H,width", [(2, 6, 4, 70), (1, 4, 16, 80), (1, 1, 16, 3000), (8, 1, 16, 700), (200, 1, 12, 90)])
+def test_tiles_of_16_rows_weigh_with_22_bits(cuda, fmt, b, T, H, width):
+    # rows in pairs of opposite codes, whose weights nearly cancel: what is left shows each weight's rounding
+    rng = np.random.default_rng(H + width + 6)
+    c = case(rng, fmt, b, T, H, width, [width] * b, [T] * b, n_rows=700, q_scale=0.01)
+    x = rng.standard_normal((350, 512)).astype(np.float32)
+    STORE[fmt](synth.f32_to_bf16_bits(np.concatenate([x, -x])), np.arange(700, dtype=np.int64), c["cache"])
+    first = np.stack([rng.permutation(350)[np.arange(width // 2) % 350] for _ in range(b)])
+    c["rows"] = np.ascontiguousarray(np.stack([first, first + 350], axis=2).reshape(b, -1)[:, rng.permutation(width // 2 * 2)]).astype(np.int32)
+    c["row_len"][:] = width // 2 * 2
+    c["masks"] = [[0] * T] * b
+    check(c, *launch(c, cuda), bits=22)

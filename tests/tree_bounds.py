@@ -9,8 +9,8 @@ rows that a node does not see, and of a row that it sees only what the row weigh
     of the exponential). A weight is off by p_j (e^ds_j - 1), out by that on |c_j| and, through the sum of the
     weights, by sum_j p_j (e^ds_j - 1) on sum_j p_j |c_j|.
   * softmax weights: the codes are multiplied with P'_j = 2^G p_j scale_j / sigma in fp16, sigma a power of two below
-    twice the largest p_j scale_j of the rows seen: off by 2^-11 relative, or by at most 2^-25 and by itself
-    when it is below 2^-14, that is by min(p_j scale_j, FLUSH max_j p_j scale_j) |code_j| of the output, FLUSH = 2^(-24 - G).
+    twice the largest p_j scale_j of the rows seen: off by 2^-11 relative (in tiles of 16 query rows a second fp16
+    number holds the rest: by 2^-22), or by at most 2^-25 and by itself when it is below 2^-14, that is by min(p_j scale_j, FLUSH max_j p_j scale_j) |code_j| of the output, FLUSH = 2^(-24 - G).
     (Weights below 2^-120 of the largest may be 0: far below that.)
   * the sums: (n / 8 + 80) u32 relative, as in tests/tree_reference.py; the output as bf16: 2^-8 relative.
 """
@@ -21,9 +21,9 @@ from tests.tree_reference import U32, row_scales, values
 FLUSH = 2.0 ** -32                                     # G = 8
 
 
-def node(q, c, scales, sm_scale, times=None):
+def node(q, c, scales, sm_scale, times=None, bits=11):
     """(out [H, 512], lse [H], allowed error of out, of lse) of a node over the rows c that it sees, each of them
-    `times` times over (None: once)."""
+    `times` times over (None: once); bits: of a softmax weight."""
     H, n = q.shape[0], c.shape[0]
     if n == 0:
         return np.zeros((H, 512)), np.full(H, -np.inf), np.zeros((H, 512)), np.zeros(H)
@@ -46,11 +46,11 @@ def node(q, c, scales, sm_scale, times=None):
     codes = np.where(scales[:, None] > 0, mag / np.where(scales > 0, scales, 1.0)[:, None], 0.0)
     w = one * scales[None]
     flush = (times * np.minimum(w, FLUSH * w.max(1, keepdims=True))) @ codes
-    tol = (2.0 ** -8 * np.abs(out) + dp @ mag + spread * (2.0 ** -11 + drift + sums)[:, None] + flush) * 1.01 + 1e-30
+    tol = (2.0 ** -8 * np.abs(out) + dp @ mag + spread * (2.0 ** -bits + drift + sums)[:, None] + flush) * 1.01 + 1e-30
     return out, lse, tol, (drift + sums) * 1.01 + 4 * U32 * np.abs(lse)
 
 
-def tree(c, sm_scale, q, batch):
+def tree(c, sm_scale, q, batch, bits=11):
     """Every node of the sequences `batch` of a case of tests/test_gpu_tree.py, as tests/tree_reference.py's tree; q: fp64.
     Drafts that nobody sees may hold anything."""
     T = q.shape[1]
@@ -65,4 +65,4 @@ def tree(c, sm_scale, q, batch):
                 continue
             see = [b * T + j for j in range(t) if (int(c["masks"][b][i]) >> j) & 1]
             yield (b, i) + node(q[b, i], np.concatenate([pre, values(c["draft"], see, c["fmt"])]),
-                                np.concatenate([psc, row_scales(c["draft"], see, c["fmt"])]), sm_scale)
+                                np.concatenate([psc, row_scales(c["draft"], see, c["fmt"])]), sm_scale, bits=bits)
