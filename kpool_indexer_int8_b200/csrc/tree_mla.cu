@@ -89,6 +89,37 @@ __device__ __forceinline__ void tr_tmem_ld(uint32_t taddr, uint32_t (&r)[V]) {
     else tc::tmem_ld32(taddr, r);
 }
 
+// The largest over a warp's keys, one a lane with scores x of V query rows and log2 scale lg, for the row that butterfly()
+// leaves in this lane.
+template <int V>
+__device__ __forceinline__ Largest largest_of(const float (&x)[V], float lg) {
+    const int lane = threadIdx.x & 31;
+    auto get = [](Largest v, int bit) { return Largest{__shfl_xor_sync(0xffffffffu, v.x, bit), __shfl_xor_sync(0xffffffffu, v.y, bit)}; };
+    Largest t[V / 2];
+    {
+        const bool up = (lane & 16) != 0;
+        const float other = __shfl_xor_sync(0xffffffffu, lg, 16);
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) {
+            const float send = up ? x[i] : x[i + V / 2], keep = up ? x[i + V / 2] : x[i];
+            t[i] = larger({keep, lg}, {__shfl_xor_sync(0xffffffffu, send, 16), other});
+        }
+    }
+#pragma unroll
+    for (int half = V / 4, bit = 8; half >= 1; half >>= 1, bit >>= 1) {
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < half; i++) {
+            const Largest send = up ? t[i] : t[i + half], keep = up ? t[i + half] : t[i];
+            t[i] = larger(keep, get(send, bit));
+        }
+    }
+    constexpr int kRest = (V == 32) ? 0 : (V == 16) ? 1 : 2;
+#pragma unroll
+    for (int k = 0; k < kRest; k++) t[0] = larger(t[0], get(t[0], 1 << (kRest - 1 - k)));
+    return t[0];
+}
+
 template <int NQ, int kFmt>
 __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(TreeArgs a, TreePlan plan, float *__restrict__ part_acc,
                                                                  float *__restrict__ part_ml) {
@@ -437,32 +468,23 @@ __global__ void __launch_bounds__(TrLayout<NQ>::kThreads, 1) tree_mla_kernel(Tre
             if (named_or(1, 256, past > kTop)) {
                 // move the references and sigmas that have to, and rescale what they scale
                 const int at = quad * NQ + c0 + ((lane >> kShift) & (V - 1));
-                float m[V];
-#pragma unroll
-                for (int e = 0; e < V; e++) m[e] = x[e];
-                const float bx = butterfly<V, true>(m), ls = mag > 0.0f ? lg : -INFINITY;
-#pragma unroll
-                for (int e = 0; e < V; e++) m[e] = x[e] + ls;
-                const float by = butterfly<V, true>(m);
+                const Largest most_here = largest_of<V>(x, mag > 0.0f ? lg : -INFINITY);
                 if ((lane & kLow) == 0) {
-                    red[at] = bx;
-                    red[4 * NQ + at] = by;
+                    red[at] = most_here.x;
+                    red[4 * NQ + at] = most_here.y;
                 }
                 named_sync(1, 256);
                 float fo = 1.0f;
                 if (tid < NQ) {
                     const float *rx = red + tid, *ry = red + 4 * NQ + tid;
-                    const float mx = fmaxf(fmaxf(rx[0], rx[NQ]), fmaxf(rx[2 * NQ], rx[3 * NQ]));
-                    const float my = fmaxf(fmaxf(ry[0], ry[NQ]), fmaxf(ry[2 * NQ], ry[3 * NQ]));
-                    const float old = fac[tid].y;
-                    Scaling s{old, log_sigma[tid], log_sigma[tid] == -INFINITY};
+                    const Largest t = larger(larger({rx[0], ry[0]}, {rx[NQ], ry[NQ]}), larger({rx[2 * NQ], ry[2 * NQ]}, {rx[3 * NQ], ry[3 * NQ]}));
+                    Scaling s{fac[tid].y, log_sigma[tid], log_sigma[tid] == -INFINITY};
                     float fl;
-                    move_scaling(s, mx, my, fl, fo);
+                    red[tid] = move_scaling(s, t, fl, fo);
                     fac[tid].y = s.ref;
                     log_sigma[tid] = s.log_sigma;
                     if (!s.none) inv[tid] = pow2f_exact(-static_cast<int>(s.log_sigma));
                     alpha[tid] = fo;
-                    red[tid] = s.ref == old ? 0.0f : s.ref - old;
                     red[4 * NQ + tid] = fl;
                 }
                 const bool rescale = named_or(1, 256, fo != 1.0f);

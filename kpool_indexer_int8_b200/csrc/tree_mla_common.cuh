@@ -335,19 +335,30 @@ struct Scaling {
     float ref, log_sigma;
     bool none;                                 // it has seen no key
 };
-// They move for a tile whose largest score is x and whose largest score plus log2 scale is y, less the reference (-infinity: no
-// key that the row sees, or scores that are NaN). What the sum so far has to be multiplied by, and the output.
-__device__ __forceinline__ void move_scaling(Scaling &s, float x, float y, float &l_factor, float &o_factor) {
+// What a tile's keys are to a query row: the largest score x, and y, the largest score plus log2 scale less x
+// (a sum of both would lose the logarithm beside a score past 2^20). A key: its score and log2 scale; -infinity, or
+// a score that is NaN: none that the row sees (y is then anything, NaN too, and passed over).
+struct Largest {
+    float x, y;
+};
+__device__ __forceinline__ Largest larger(Largest a, Largest b) {
+    const float x = fmaxf(a.x, b.x);
+    return {x, fmaxf(a.y + (a.x - x), b.y + (b.x - x))};
+}
+// The scaling moves for them. Returns by how much the reference does, and what the sum so far and the output have
+// to be multiplied by.
+__device__ __forceinline__ float move_scaling(Scaling &s, Largest t, float &l_factor, float &o_factor) {
     l_factor = o_factor = 1.0f;
-    if (!(x > -INFINITY)) return;
-    const float ref = s.none || x > kHead ? s.ref + ceilf(x - kHead) : s.ref, delta = s.ref == ref ? 0.0f : ref - s.ref;
-    float sigma = fminf(fmaxf(ceilf(y - delta - kHead), -126.0f), 126.0f);
+    if (!(t.x > -INFINITY)) return 0.0f;
+    const float delta = s.none || t.x > kHead ? ceilf(t.x - kHead) : 0.0f, y = t.y + (t.x - delta);
+    float sigma = fminf(fmaxf(ceilf(y - kHead), -126.0f), 126.0f);
     if (!s.none) {
         sigma = delta == 0.0f && y - s.log_sigma <= kTop ? s.log_sigma : fmaxf(s.log_sigma - delta, sigma);
         l_factor = pow2_whole(-delta);
         o_factor = pow2_whole(s.log_sigma - sigma - delta);
     }
-    s = {ref, sigma, false};
+    s = {s.ref + delta, sigma, false};
+    return delta;
 }
 // 8 bf16 values times f as 8 fp16 values.
 __device__ __forceinline__ uint4 bf16_to_f16x8(const uint4 &v, float f) {

@@ -489,22 +489,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrThreads, 1)
             for (int e = 0; e < kPrHalf; e += 2) mx = max3(mx, x[e], x[e + 1]);
             if (named_or(1, 32 * kPrSoft, mx > most)) {
                 // the scaling of the rows moves, where it has to, and what it scales is rescaled
-                float my = -INFINITY;
+                float my = -INFINITY;                                   // (of the scores less mx)
                 const float4 *lg4 = reinterpret_cast<const float4 *>(slog + m * kPrKeys + key0);
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e += 4) {
                     const float4 lg = lg4[e >> 2];
-                    my = max3(max3(my, x[e] + lg.x, x[e + 1] + lg.y), x[e + 2] + lg.z, x[e + 3] + lg.w);
+                    my = max3(max3(my, (x[e] - mx) + lg.x, (x[e + 1] - mx) + lg.y), (x[e + 2] - mx) + lg.z, (x[e + 3] - mx) + lg.w);
                 }
                 red2[mine] = make_float2(mx, my);
                 named_sync(1, 32 * kPrSoft);
                 const float2 o = red2[other];
-                const float old = scaling.ref;
                 float fl, fo;
-                move_scaling(scaling, fmaxf(mx, o.x), fmaxf(my, o.y), fl, fo);
+                const float delta = move_scaling(scaling, larger({mx, my}, {o.x, o.y}), fl, fo);
                 inv = pow2f_exact(-static_cast<int>(scaling.log_sigma));
                 l *= fl;
-                const float delta = scaling.ref == old ? 0.0f : scaling.ref - old;
 #pragma unroll
                 for (int e = 0; e < kPrHalf; e++) x[e] -= delta;
                 if (i > 0 && __any_sync(0xffffffffu, fo != 1.0f)) {

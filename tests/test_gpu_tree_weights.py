@@ -174,3 +174,31 @@ def test_tiles_of_16_rows_weigh_with_22_bits(cuda, fmt, b, T, H, width):
     c["row_len"][:] = width // 2 * 2
     c["masks"] = [[0] * T] * b
     check(c, *launch(c, cuda), bits=22)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 24, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("first", [True, False])
+def test_a_row_that_weighs_everything(cuda, fmt, cut, ratio, first):
+    # a row far above the others in scale and score: the output is that row, from the first tile on or after others
+    b, T, H, width = cut
+    rng = np.random.default_rng(H + width + 7)
+    c = case(rng, fmt, b, T, H, width, [width] * b, [T] * b, n_rows=700)
+    c["q"] = synth.f32_to_bf16_bits(synth.bf16_bits_to_f32(c["q"]) + np.float32(0.5))
+    raw = c["cache"].view(np.uint8)
+    raw[7, :256 if fmt == "fp4" else 512] = {"int8": 0x64, "fp8": 0x7E, "fp4": 0x22}[fmt]
+    if fmt == "fp4":
+        raw[7, 256:288] = 0x7E
+    c["rows"][c["rows"] == 7] = 8
+    c["rows"][:, 0 if first else width // 2] = 7
+    set_scale(c["cache"], [7], fmt, float(np.median(R.row_scales(c["cache"], np.arange(700), fmt))) * ratio)
+    row = R.values(c["cache"], [7], fmt)[0]
+    s = synth.bf16_bits_to_f32(c["q"]).astype(np.float64) @ row * SM
+    assert s.min() > 300.0                                        # (any other row's e^-150 and less beside it)
+    out, lse = launch(c, cuda)
+    o, l = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    # the output: 2^-11 of the weight, 2^-8 of bf16; lse: 520 half steps of the sum of |q c|, all of one sign but for q's
+    assert (np.abs(o - row) <= 1.01 * (2.0 ** -8 + 2.0 ** -11) * np.abs(row)).all()
+    mag = np.abs(synth.bf16_bits_to_f32(c["q"]).astype(np.float64)) @ np.abs(row) * SM
+    assert (np.abs(l - s) <= 1.01 * (520 * R.U32 * mag + 8 * R.U32 * np.abs(s))).all()
