@@ -16,12 +16,12 @@
 //   * warp 14 of the first CTA (tensor cores): S(t + 1), then O of t, for both CTAs.
 // K, V and P have one buffer each: shared memory holds no more beside Q.
 //
-// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,690 cycles of a CTA. The tensor cores read 172 KB of
+// What bounds it: shared memory's 128 bytes a cycle. A tile takes 3,710 cycles of a CTA. The tensor cores read 172 KB of
 // operands (Q 64, K 48, V 48, P 12), 1,380 cycles; the warps' own bytes (rows copied in and read, 49 KB each way, K
-// and V 48 KB each and P 12 KB written) are 1,650, with scales, barriers and partials 1,870 wavefronts, and 310 more are
+// and V 48 KB each and P 12 KB written) are 1,650, with scales, barriers and partials 1,870 wavefronts, and 320 more are
 // counted as bank conflicts, whose cause is not known (the addresses here have none). Tensor pipe 42 % active,
-// issue 47 %. 8 nodes of 64 heads over 262,144 int8 rows: 386 us a call back to back, under the power limit, 350 and
-// 785 TFLOP/s one at a time, 0.48 of the measured bf16 rate. What was tried on top of it and did not pay (against 369 then):
+// issue 47 %. 8 nodes of 64 heads over 262,144 int8 rows: 383 us a call back to back, under the power limit, 348 and
+// 790 TFLOP/s one at a time, 0.48 of the measured bf16 rate. What was tried on top of it and did not pay (against 369 then):
 // two teams of softmax warps on alternate tiles (410 us), eight softmax warps on one tile (386), rows read
 // in rolled loops right before they are widened (390-404), one set of warps for K and V (391), P read for each of its
 // two products (372), P' tested for fp16's range after the exponentials with the scores read again to move (389).
